@@ -23,7 +23,8 @@
  *   - GPU work is launched asynchronously on `stream` (a cudaStream_t;
  *     NULL is the legacy default stream). No call synchronises, except
  *     pa_get_device_error. pa_decode, pa_decode_append, pa_prefill,
- *     pa_reshape_and_cache, pa_copy_blocks and pa_swap_blocks can therefore
+ *     pa_reshape_and_cache, pa_rope_and_cache, pa_extend_tables,
+ *     pa_release_tables, pa_copy_blocks and pa_swap_blocks can therefore
  *     be captured in a CUDA graph and replayed; the split path's workspace
  *     must then stay allocated for the graph's lifetime.
  *   - Arguments are checked on the host before anything is launched; on a
@@ -77,6 +78,11 @@ typedef enum { PA_KV_BF16 = 0, PA_KV_FP8_E4M3 = 1 } pa_kv_dtype;
 #define PA_DEVERR_WAIT_TIMEOUT 0x8u  /* decode: a staging wait gave up       */
 #define PA_DEVERR_BLOCK_RANGE 0x10u  /* decode: table id outside the pool    */
                                      /* (that block was read as zeros)      */
+#define PA_DEVERR_OUT_OF_BLOCKS 0x20u /* extend: the free stack is too short */
+#define PA_DEVERR_LENGTH_RANGE 0x40u /* extend, release: a negative length,  */
+                                     /* one past the table, too many tokens  */
+#define PA_DEVERR_FREE_RANGE 0x80u   /* extend, release: free count outside  */
+                                     /* its array, or a push past its end    */
 
 /* Human-readable name of a status. Never NULL; static storage. */
 PA_API const char *pa_status_string(pa_status status);
@@ -258,6 +264,144 @@ PA_API pa_status pa_reshape_and_cache(const void *key, const void *value,
                                int num_kv_heads, int head_dim, int block_size,
                                int num_blocks, pa_kv_dtype kv_dtype,
                                float k_scale, float v_scale, void *stream);
+
+/* How pa_rope_frequencies stretches the frequencies for long contexts. With
+ * f_i = base^(-2i / rotary_dim):
+ *   PA_ROPE_NONE    f_i.
+ *   PA_ROPE_LINEAR  f_i / factor (positions interpolated).
+ *   PA_ROPE_BASE    f_i of the base base * factor^(r / (r - 2)), r =
+ *                   rotary_dim: the slowest component is divided by factor,
+ *                   the fastest kept.
+ *   PA_ROPE_BANDS   by wavelength against the original context N: with
+ *                   x = (N f_i / 2 pi - low) / (high - low) clamped to
+ *                   [0, 1], f_i (x + (1 - x) / factor): components that turn
+ *                   at least `high` times in N tokens are kept, those that
+ *                   turn at most `low` times are divided by factor.
+ *   PA_ROPE_YARN    the method published as YaRN: a ramp over the component
+ *                   index between the components that turn `high` and `low`
+ *                   times in N tokens (rounded outwards), and rope_scale =
+ *                   0.1 ln(factor) + 1 on the rotated values. */
+typedef enum {
+  PA_ROPE_NONE = 0,
+  PA_ROPE_LINEAR = 1,
+  PA_ROPE_BASE = 2,
+  PA_ROPE_BANDS = 3,
+  PA_ROPE_YARN = 4
+} pa_rope_scaling;
+
+/* The table pa_rope_and_cache reads: inv_freq_out fp64 [rotary_dim / 2]
+ * (HOST) receives the angles per position in radians, *rope_scale_out (host)
+ * the factor on the rotated values (1 except for PA_ROPE_YARN). rotary_dim:
+ * a positive even number (above 2 for PA_ROPE_BASE); base > 1; factor >= 1
+ * (not read for NONE); original_max_position > 0 and 0 < low < high for
+ * BANDS and YARN (not read otherwise). Anything else: PA_ERR_INVALID_ARG. */
+PA_API pa_status pa_rope_frequencies(double *inv_freq_out, float *rope_scale_out,
+                                     int rotary_dim, double base,
+                                     pa_rope_scaling scaling, double factor,
+                                     double original_max_position, double low,
+                                     double high);
+
+/* Rotary positions of a step's queries and keys, and the rotated keys and
+ * the values into their cache slots, in one launch: what the projections
+ * give goes in, what pa_decode / pa_prefill read comes out. With r =
+ * rotary_dim, pair i (0 <= i < r / 2) of a head is its elements (i, i + r/2),
+ * or (2i, 2i + 1) when interleaved is non-zero; elements r .. head_dim - 1
+ * pass through. For token t and theta = positions[t] * inv_freq[i]:
+ *     (a, b) -> rope_scale * (a cos theta - b sin theta,
+ *                             b cos theta + a sin theta)
+ * in fp32 with the angle reduced exactly (any int32 position keeps full
+ * precision), rounded once: q_out to bf16, keys to the cache type. Values
+ * and unrotated key elements are stored as pa_reshape_and_cache stores them.
+ *   q_out          bf16 [num_tokens][num_q_heads][head_dim], 16-byte aligned.
+ *                  May be q itself when q_stride = num_q_heads * head_dim;
+ *                  no other overlap with the inputs.
+ *   q, key, value  bf16, a token's heads contiguous, tokens q_stride /
+ *                  k_stride / v_stride elements apart (>= heads * head_dim,
+ *                  multiples of 8): contiguous tensors or views of one fused
+ *                  projection. 16-byte aligned.
+ *   k_cache, v_cache, slot_mapping, kv_dtype, k_scale, v_scale  as for
+ *                  pa_reshape_and_cache; a token with slot < 0 has its query
+ *                  rotated and nothing cached.
+ *   positions      int32 [num_tokens], device; any value.
+ *   inv_freq       fp64 [rotary_dim / 2], device, finite (8-byte aligned).
+ *   rotary_dim     a multiple of 16 in [16, head_dim]; others return
+ *                  PA_ERR_UNSUPPORTED.
+ *   rope_scale     finite. */
+PA_API pa_status pa_rope_and_cache(void *q_out, const void *q, const void *key,
+                                   const void *value, void *k_cache, void *v_cache,
+                                   const int64_t *slot_mapping,
+                                   const int32_t *positions, const double *inv_freq,
+                                   int rotary_dim, int interleaved, float rope_scale,
+                                   int64_t q_stride, int64_t k_stride,
+                                   int64_t v_stride, int num_tokens, int num_q_heads,
+                                   int num_kv_heads, int head_dim, int block_size,
+                                   int num_blocks, pa_kv_dtype kv_dtype,
+                                   float k_scale, float v_scale, void *stream);
+
+/* ------------------------------------------------- block tables on the GPU - */
+
+/* Block tables, slots and positions of a step, built on the GPU from the
+ * rows' lengths. The free blocks are a stack in device memory:
+ * free_blocks[0 .. *free_count) are block ids, the top is the last. For row
+ * s with L = context_lens[s] tokens and n = new_lens[s] new ones, in row
+ * order: ceil((L + n) / 16) - ceil(L / 16) blocks are popped and written
+ * behind the row's table entries, and its n tokens take the next rows of
+ * slot_mapping and positions (slot table[p / 16] * 16 + p % 16 at position
+ * p = L, L + 1, ...). What pa_pool_append does on the host, for rows whose
+ * last, partly filled block is theirs alone (no copy-on-write): a step that
+ * uses it needs no upload and can be captured in a CUDA graph whole.
+ *   block_tables   int32 [num_seqs][max_blocks_per_seq]; only the new entries
+ *                  are written.
+ *   context_lens, free_count          read; int32 [num_seqs], int32 [1].
+ *   context_lens_out, free_count_out  L + n and the count left; may be the
+ *                  inputs themselves (updated in place).
+ *   new_lens       int32 [num_seqs], >= 0; 0 leaves the row alone.
+ *   free_blocks    int32 [free_capacity], read.
+ *   slot_mapping   int64 [num_tokens], positions int32 [num_tokens]: rows
+ *                  behind the last new token get slot -1 and position 0 (a
+ *                  batch padded to num_tokens, as pa_reshape_and_cache and
+ *                  pa_rope_and_cache skip it).
+ *   query_start    int32 [num_seqs + 1]: exclusive sums of new_lens, as
+ *                  pa_prefill takes them.
+ * All or nothing: too few free blocks (PA_DEVERR_OUT_OF_BLOCKS), a negative
+ * length, a row past its table, more than num_tokens tokens
+ * (PA_DEVERR_LENGTH_RANGE) or a count outside [0, free_capacity]
+ * (PA_DEVERR_FREE_RANGE) leave tables, lengths and count as they were, with
+ * every slot -1, positions and query_start 0. A block id outside
+ * [0, num_blocks) gives slot -1 (PA_DEVERR_BLOCK_RANGE). num_seqs up to 16384
+ * (more: PA_ERR_UNSUPPORTED). Other pointers 4-byte aligned, slot_mapping 8. */
+PA_API pa_status pa_extend_tables(int32_t *block_tables, int max_blocks_per_seq,
+                                  const int32_t *context_lens,
+                                  const int32_t *new_lens,
+                                  const int32_t *free_blocks, int free_capacity,
+                                  const int32_t *free_count,
+                                  int32_t *context_lens_out,
+                                  int32_t *free_count_out, int64_t *slot_mapping,
+                                  int32_t *positions, int32_t *query_start,
+                                  int num_seqs, int num_tokens, int block_size,
+                                  int num_blocks, void *stream);
+
+/* The end of rows: for every row s with release[s] != 0, in row order, the
+ * blocks behind its first keep_blocks (a prefix it shares and does not own)
+ * are pushed on the free stack in table order, and its length becomes
+ * min(L, 16 * keep_blocks): the row is ready for the next request behind the
+ * same prefix (0 for an empty row). Other rows keep their lengths.
+ * block_tables is only read (entries past a row's length mean nothing).
+ *   free_blocks    int32 [free_capacity], entries from *free_count on written.
+ *   context_lens_out, free_count_out  may be the inputs themselves.
+ * All or nothing: a released length below 0 or past the table
+ * (PA_DEVERR_LENGTH_RANGE), a count outside [0, free_capacity] or a push past
+ * free_capacity (PA_DEVERR_FREE_RANGE) leave lengths, count and stack as they
+ * were. An id outside the pool is pushed and flagged PA_DEVERR_BLOCK_RANGE. */
+PA_API pa_status pa_release_tables(const int32_t *block_tables,
+                                   int max_blocks_per_seq,
+                                   const int32_t *context_lens,
+                                   const int32_t *release, int32_t *free_blocks,
+                                   int free_capacity, const int32_t *free_count,
+                                   int32_t *context_lens_out,
+                                   int32_t *free_count_out, int keep_blocks,
+                                   int num_seqs, int block_size, int num_blocks,
+                                   void *stream);
 
 /* Copy-on-write block copies: for each pair (src, dst), copy physical block
  * src to dst in both caches. Sharers of a prefix point at the same blocks;

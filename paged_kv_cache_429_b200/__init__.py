@@ -8,6 +8,10 @@ functions carry the names of the C entry points (include/pa.h):
     pa_decode_append        the same with the step's new tokens written to their slots in-kernel
     pa_prefill              chunked causal prefill attention through block tables
     pa_reshape_and_cache    scatter new K/V into cache slots (bf16 / fp8)
+    pa_rope_and_cache       rotary positions of q and k, with the cache write in the same launch
+    pa_rope_frequencies     its frequency table (plain or stretched for long contexts)
+    pa_extend_tables        block tables, slots and positions built on the GPU from request lengths
+    pa_release_tables       finished rows' blocks back to the device-resident free stack
     pa_copy_blocks          copy-on-write block copies
     pa_swap_blocks          block copies between the GPU cache and pinned host memory
     pa_decode_no_alloc      split-context decode with the library's fixed scratch
@@ -31,13 +35,16 @@ from ._lib import STATUS_NAMES, LibraryNotBuilt
 __all__ = [
     "PA_KV_BF16", "PA_KV_FP8_E4M3", "BLOCK_SIZE", "PagedAttentionError",
     "LibraryNotBuilt", "pa_decode", "pa_decode_append", "pa_decode_no_alloc", "pa_prefill", "pa_reshape_and_cache", "pa_copy_blocks",
-    "pa_swap_blocks", "pa_decode_workspace_size", "pa_get_device_error",
-    "pa_status_string",
+    "pa_swap_blocks", "pa_rope_and_cache", "pa_rope_frequencies", "pa_extend_tables",
+    "pa_release_tables", "pa_decode_workspace_size", "pa_get_device_error",
+    "pa_status_string", "PA_ROPE_NONE", "PA_ROPE_LINEAR", "PA_ROPE_BASE", "PA_ROPE_BANDS",
+    "PA_ROPE_YARN",
     "BlockPool", "kv_dtype_of",
 ]
 
 PA_KV_BF16 = 0
 PA_KV_FP8_E4M3 = 1
+PA_ROPE_NONE, PA_ROPE_LINEAR, PA_ROPE_BASE, PA_ROPE_BANDS, PA_ROPE_YARN = range(5)
 BLOCK_SIZE = 16
 
 
@@ -272,6 +279,154 @@ def pa_reshape_and_cache(key: torch.Tensor, value: torch.Tensor,
             slot_mapping.data_ptr(), T, Hkv, D, B, NB, kv_dtype_of(k_cache),
             float(k_scale), float(v_scale), _stream_ptr(stream, key.device))
     _ok(rc, "pa_reshape_and_cache")
+
+
+def pa_rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: int = PA_ROPE_NONE, *,
+                        factor: float = 1.0, original_max_position: float = 0.0,
+                        low: float = 1.0, high: float = 32.0, device=None):
+    """The frequency table of pa_rope_and_cache (see pa.h for the scalings):
+    (inv_freq fp64 [rotary_dim / 2] on `device`, rope_scale)."""
+    inv = torch.empty(max(int(rotary_dim), 0) // 2, dtype=torch.float64)
+    scale = ctypes.c_float(0.0)
+    _ok(_lib.lib().pa_rope_frequencies(inv.data_ptr() or None, ctypes.byref(scale), int(rotary_dim),
+                                       float(base), int(scaling), float(factor),
+                                       float(original_max_position), float(low), float(high)),
+        "pa_rope_frequencies")
+    return (inv if device is None else inv.to(device)), float(scale.value)
+
+
+def _need_rows(t: torch.Tensor, name: str):
+    """bf16 [tokens][heads][head_dim] with each token's heads contiguous; any
+    token stride (a view of a fused projection)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name}: dtype {t.dtype} not in {(torch.bfloat16,)}")
+    if t.dim() != 3:
+        raise ValueError(f"{name}: expected 3 dims, got {tuple(t.shape)}")
+    if not (t.stride(2) == 1 and (t.stride(1) == t.shape[2] or t.shape[1] == 1)):
+        raise ValueError(f"{name}: each token's heads must be contiguous")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    # of a single token the stride says nothing
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def pa_rope_and_cache(q_out: torch.Tensor, q: torch.Tensor, key: torch.Tensor,
+                      value: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                      slot_mapping: torch.Tensor, positions: torch.Tensor,
+                      inv_freq: torch.Tensor, *, interleaved: bool = False,
+                      rope_scale: float = 1.0, k_scale: float = 1.0, v_scale: float = 1.0,
+                      stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Rotate q and key by their positions (see pa.h): q_out [T][Hq][D] bf16
+    is written in place (it may be q), the rotated keys and the values go to
+    their slots of the caches. q, key, value may be views with a token
+    stride; the rotated part of a head is its first 2 * len(inv_freq)
+    elements."""
+    _need(q_out, "q_out", (torch.bfloat16,), 3)
+    _need_rows(q, "q")
+    _need_rows(key, "key")
+    _need_rows(value, "value")
+    _need(k_cache, "k_cache", (torch.bfloat16, torch.float8_e4m3fn, torch.uint8), 4)
+    _need(v_cache, "v_cache", (k_cache.dtype,), 4)
+    _need(slot_mapping, "slot_mapping", (torch.int64,), 1)
+    _need(positions, "positions", (torch.int32,), 1)
+    _need(inv_freq, "inv_freq", (torch.float64,), 1)
+    T, Hq, D = q.shape
+    NB, Hkv, B, Dc = k_cache.shape
+    if tuple(q_out.shape) != (T, Hq, D) or Dc != D or tuple(v_cache.shape) != tuple(k_cache.shape):
+        raise ValueError("shape mismatch between q_out, q and the caches")
+    if tuple(key.shape) != (T, Hkv, D) or tuple(value.shape) != (T, Hkv, D):
+        raise ValueError("key / value must be [num_tokens][num_kv_heads][head_dim]")
+    if slot_mapping.shape[0] != T or positions.shape[0] != T:
+        raise ValueError("slot_mapping / positions must have num_tokens entries")
+    with torch.cuda.device(_device_of(q_out, q, key, value, k_cache, v_cache, slot_mapping,
+                                      positions, inv_freq)):
+        rc = _lib.lib().pa_rope_and_cache(
+            q_out.data_ptr(), q.data_ptr(), key.data_ptr(), value.data_ptr(), k_cache.data_ptr(),
+            v_cache.data_ptr(), slot_mapping.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(),
+            2 * inv_freq.shape[0], int(bool(interleaved)), float(rope_scale), _row_stride(q),
+            _row_stride(key), _row_stride(value), T, Hq, Hkv, D, B, NB, kv_dtype_of(k_cache),
+            float(k_scale), float(v_scale), _stream_ptr(stream, q.device))
+    _ok(rc, "pa_rope_and_cache")
+    return q_out
+
+
+def pa_extend_tables(block_tables: torch.Tensor, context_lens: torch.Tensor,
+                     new_lens: torch.Tensor, free_blocks: torch.Tensor,
+                     free_count: torch.Tensor, context_lens_out: torch.Tensor,
+                     free_count_out: torch.Tensor, slot_mapping: torch.Tensor,
+                     positions: torch.Tensor, query_start: torch.Tensor, *,
+                     num_blocks: Optional[int] = None,
+                     stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Give every row its new tokens (see pa.h): blocks popped from the free
+    stack into block_tables [S][W], the new lengths and count (in place if
+    the same tensors are given), slots, positions and query_start of the
+    tokens. num_blocks: the pool's size (default: free_blocks' length)."""
+    _need(block_tables, "block_tables", (torch.int32,), 2)
+    _need(context_lens, "context_lens", (torch.int32,), 1)
+    _need(new_lens, "new_lens", (torch.int32,), 1)
+    _need(free_blocks, "free_blocks", (torch.int32,), 1)
+    _need(free_count, "free_count", (torch.int32,), 1)
+    _need(context_lens_out, "context_lens_out", (torch.int32,), 1)
+    _need(free_count_out, "free_count_out", (torch.int32,), 1)
+    _need(slot_mapping, "slot_mapping", (torch.int64,), 1)
+    _need(positions, "positions", (torch.int32,), 1)
+    _need(query_start, "query_start", (torch.int32,), 1)
+    S, W = block_tables.shape
+    T = slot_mapping.shape[0]
+    if context_lens.shape[0] != S or new_lens.shape[0] != S or context_lens_out.shape[0] != S:
+        raise ValueError("context_lens / new_lens must have num_seqs rows")
+    if free_count.shape[0] != 1 or free_count_out.shape[0] != 1:
+        raise ValueError("free_count must have one element")
+    if positions.shape[0] != T or query_start.shape[0] != S + 1:
+        raise ValueError("positions must have num_tokens entries, query_start num_seqs + 1")
+    nb = free_blocks.shape[0] if num_blocks is None else int(num_blocks)
+    with torch.cuda.device(_device_of(block_tables, context_lens, new_lens, free_blocks, free_count,
+                                      context_lens_out, free_count_out, slot_mapping, positions,
+                                      query_start)):
+        rc = _lib.lib().pa_extend_tables(
+            block_tables.data_ptr(), W, context_lens.data_ptr(), new_lens.data_ptr(),
+            free_blocks.data_ptr(), free_blocks.shape[0], free_count.data_ptr(),
+            context_lens_out.data_ptr(), free_count_out.data_ptr(), slot_mapping.data_ptr(),
+            positions.data_ptr(), query_start.data_ptr(), S, T, BLOCK_SIZE, nb,
+            _stream_ptr(stream, block_tables.device))
+    _ok(rc, "pa_extend_tables")
+
+
+def pa_release_tables(block_tables: torch.Tensor, context_lens: torch.Tensor,
+                      release: torch.Tensor, free_blocks: torch.Tensor,
+                      free_count: torch.Tensor, context_lens_out: torch.Tensor,
+                      free_count_out: torch.Tensor, *, keep_blocks: int = 0,
+                      num_blocks: Optional[int] = None,
+                      stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Push the blocks of the rows with release != 0, behind their first
+    keep_blocks, on the free stack (see pa.h); lengths and count as for
+    pa_extend_tables."""
+    _need(block_tables, "block_tables", (torch.int32,), 2)
+    _need(context_lens, "context_lens", (torch.int32,), 1)
+    _need(release, "release", (torch.int32,), 1)
+    _need(free_blocks, "free_blocks", (torch.int32,), 1)
+    _need(free_count, "free_count", (torch.int32,), 1)
+    _need(context_lens_out, "context_lens_out", (torch.int32,), 1)
+    _need(free_count_out, "free_count_out", (torch.int32,), 1)
+    S, W = block_tables.shape
+    if context_lens.shape[0] != S or release.shape[0] != S or context_lens_out.shape[0] != S:
+        raise ValueError("context_lens / release must have num_seqs rows")
+    if free_count.shape[0] != 1 or free_count_out.shape[0] != 1:
+        raise ValueError("free_count must have one element")
+    nb = free_blocks.shape[0] if num_blocks is None else int(num_blocks)
+    with torch.cuda.device(_device_of(block_tables, context_lens, release, free_blocks, free_count,
+                                      context_lens_out, free_count_out)):
+        rc = _lib.lib().pa_release_tables(
+            block_tables.data_ptr(), W, context_lens.data_ptr(), release.data_ptr(),
+            free_blocks.data_ptr(), free_blocks.shape[0], free_count.data_ptr(),
+            context_lens_out.data_ptr(), free_count_out.data_ptr(), int(keep_blocks), S, BLOCK_SIZE,
+            nb, _stream_ptr(stream, block_tables.device))
+    _ok(rc, "pa_release_tables")
 
 
 def pa_copy_blocks(k_cache: torch.Tensor, v_cache: torch.Tensor,

@@ -20,6 +20,7 @@ STATUS_NAMES = {
 # Every function the header declares, with (restype, argtypes).
 _i32, _i64, _u64 = ctypes.c_int, ctypes.c_int64, ctypes.c_uint64
 _f32, _vp, _sz = ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t
+_f64 = ctypes.c_double
 SIGNATURES = {
     "pa_status_string": (ctypes.c_char_p, [_i32]),
     "pa_decode_workspace_size": (_sz, [_i32, _i32, _i32, _i32, _i32]),
@@ -36,6 +37,15 @@ SIGNATURES = {
                           _i32, _i32, _i32, _i32, _i32, _i32, _f32, _vp]),
     "pa_reshape_and_cache": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32,
                                     _i32, _i32, _i32, _f32, _f32, _vp]),
+    "pa_rope_frequencies": (_i32, [_vp, ctypes.POINTER(_f32), _i32, _f64, _i32, _f64, _f64,
+                                   _f64, _f64]),
+    "pa_rope_and_cache": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _f32,
+                                 _i64, _i64, _i64, _i32, _i32, _i32, _i32, _i32, _i32, _i32,
+                                 _f32, _f32, _vp]),
+    "pa_extend_tables": (_i32, [_vp, _i32, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp,
+                                _i32, _i32, _i32, _i32, _vp]),
+    "pa_release_tables": (_i32, [_vp, _i32, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _i32, _i32,
+                                 _i32, _i32, _vp]),
     "pa_copy_blocks": (_i32, [_vp, _vp, _vp, _i32, _sz, _i32, _vp]),
     "pa_swap_blocks": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _sz, _i32, _i32, _vp]),
     "pa_get_device_error": (_i32, [ctypes.POINTER(ctypes.c_uint32)]),

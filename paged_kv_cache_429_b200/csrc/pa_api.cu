@@ -15,6 +15,8 @@
 #include "decode.cuh"
 #include "decode_tc.cuh"
 #include "prefill.cuh"
+#include "rope.cuh"
+#include "tables.cuh"
 
 namespace {
 
@@ -210,6 +212,37 @@ size_t workspace_bytes_for(int num_seqs, int num_q_heads, int head_dim, int max_
   const int64_t floats = static_cast<int64_t>(num_seqs) * num_q_heads * P * (head_dim + 2);
   const int64_t bytes = floats * 4 + 2 * 256;  // two sub-array alignments
   return static_cast<size_t>((bytes + 255) / 256 * 256);
+}
+
+template <int D, bool FP8>
+pa_status launch_rope(const pa::RopeParams &p, bool interleaved, cudaStream_t st) {
+  const int64_t ctas = (static_cast<int64_t>(p.num_tokens) + pa::kRopeTokens - 1) / pa::kRopeTokens;
+  if (interleaved)
+    pa::rope_and_cache_kernel<D, FP8, true><<<static_cast<unsigned>(ctas), pa::kRopeThreads, 0, st>>>(p);
+  else
+    pa::rope_and_cache_kernel<D, FP8, false><<<static_cast<unsigned>(ctas), pa::kRopeThreads, 0, st>>>(p);
+  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+// One cluster of pa::kTabCluster CTAs, the rows' sums in dynamic shared memory.
+template <typename Params>
+pa_status launch_table_kernel(void (*kern)(Params), const Params &p, int num_seqs,
+                                     std::atomic<uint64_t> &attr_done, cudaStream_t st) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return PA_ERR_CUDA;
+  if (!ensure_smem_attr(kern, (pa::kTabMaxSeqs + 1) * sizeof(int32_t), attr_done, dev)) return PA_ERR_CUDA;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(pa::kTabCluster);
+  cfg.blockDim = dim3(pa::kTabThreads);
+  cfg.dynamicSmemBytes = (static_cast<size_t>(num_seqs) + 1) * sizeof(int32_t);
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = pa::kTabCluster;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 }  // namespace
@@ -538,6 +571,185 @@ pa_status pa_reshape_and_cache(const void *key, const void *value, void *k_cache
         slot_mapping, total, chunks_per_token, chunks_per_row, num_kv_heads, head_dim, num_slots,
         k_scale, v_scale);
   return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+pa_status pa_rope_frequencies(double *inv_freq_out, float *rope_scale_out, int rotary_dim,
+                              double base, pa_rope_scaling scaling, double factor,
+                              double original_max_position, double low, double high) {
+  if (!inv_freq_out || !rope_scale_out || rotary_dim <= 0 || rotary_dim % 2 != 0 ||
+      !(std::isfinite(base) && base > 1.0))
+    return PA_ERR_INVALID_ARG;
+  if (scaling < PA_ROPE_NONE || scaling > PA_ROPE_YARN) return PA_ERR_INVALID_ARG;
+  if (scaling != PA_ROPE_NONE && !(std::isfinite(factor) && factor >= 1.0)) return PA_ERR_INVALID_ARG;
+  if (scaling == PA_ROPE_BASE && rotary_dim <= 2) return PA_ERR_INVALID_ARG;
+  const bool ramped = scaling == PA_ROPE_BANDS || scaling == PA_ROPE_YARN;
+  if (ramped && !(std::isfinite(original_max_position) && original_max_position > 0.0 && low > 0.0 &&
+                  std::isfinite(high) && high > low))
+    return PA_ERR_INVALID_ARG;
+  const double r = rotary_dim, two_pi = 2.0 * std::acos(-1.0);
+  if (scaling == PA_ROPE_BASE) base *= std::pow(factor, r / (r - 2.0));
+  // YaRN's ramp: the (real-valued) component that turns `turns` times in the
+  // original context, N base^(-2i/r) / 2 pi = turns
+  double lo = 0.0, hi = 1.0;
+  if (scaling == PA_ROPE_YARN) {
+    const auto component = [&](double turns) {
+      return r * std::log(original_max_position / (turns * two_pi)) / (2.0 * std::log(base));
+    };
+    lo = std::max(std::floor(component(high)), 0.0);
+    hi = std::min(std::ceil(component(low)), r - 1.0);
+  }
+  for (int i = 0; i < rotary_dim / 2; ++i) {
+    const double f = std::pow(base, -2.0 * i / r);
+    double keep = 1.0;  // share of the unscaled frequency
+    if (scaling == PA_ROPE_LINEAR) keep = 0.0;
+    if (scaling == PA_ROPE_BANDS)
+      keep = (original_max_position * f / two_pi - low) / (high - low);
+    if (scaling == PA_ROPE_YARN) keep = 1.0 - (i - lo) / std::max(hi - lo, 1e-3);
+    keep = std::min(std::max(keep, 0.0), 1.0);
+    inv_freq_out[i] = keep == 1.0 ? f : f * (keep + (1.0 - keep) / factor);
+  }
+  *rope_scale_out = scaling == PA_ROPE_YARN ? static_cast<float>(0.1 * std::log(factor) + 1.0) : 1.f;
+  return PA_OK;
+}
+
+pa_status pa_rope_and_cache(void *q_out, const void *q, const void *key, const void *value,
+                            void *k_cache, void *v_cache, const int64_t *slot_mapping,
+                            const int32_t *positions, const double *inv_freq, int rotary_dim,
+                            int interleaved, float rope_scale, int64_t q_stride, int64_t k_stride,
+                            int64_t v_stride, int num_tokens, int num_q_heads, int num_kv_heads,
+                            int head_dim, int block_size, int num_blocks, pa_kv_dtype kv_dtype,
+                            float k_scale, float v_scale, void *stream) {
+  if (num_tokens < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || num_blocks <= 0 ||
+      rotary_dim <= 0)
+    return PA_ERR_INVALID_ARG;
+  if (kv_dtype != PA_KV_BF16 && kv_dtype != PA_KV_FP8_E4M3) return PA_ERR_INVALID_ARG;
+  if (block_size != pa::kBS) return PA_ERR_UNSUPPORTED;
+  if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
+  if (rotary_dim > head_dim || rotary_dim % 16 != 0) return PA_ERR_UNSUPPORTED;
+  // unit counts of a CTA's tokens stay inside 32 bits
+  if (num_q_heads > 65535 || num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;
+  if (!std::isfinite(rope_scale)) return PA_ERR_INVALID_ARG;
+  if (kv_dtype == PA_KV_FP8_E4M3 &&
+      !(std::isfinite(k_scale) && k_scale > 0.f && std::isfinite(v_scale) && v_scale > 0.f))
+    return PA_ERR_INVALID_ARG;
+  const int64_t q_row = static_cast<int64_t>(num_q_heads) * head_dim;
+  const int64_t kv_row = static_cast<int64_t>(num_kv_heads) * head_dim;
+  if (q_stride < q_row || k_stride < kv_row || v_stride < kv_row || q_stride % 8 != 0 ||
+      k_stride % 8 != 0 || v_stride % 8 != 0)
+    return PA_ERR_INVALID_ARG;
+  if (num_tokens == 0) return PA_OK;
+  if (!q_out || !q || !key || !value || !k_cache || !v_cache || !slot_mapping || !positions || !inv_freq)
+    return PA_ERR_INVALID_ARG;
+  if (!aligned(q_out, 16) || !aligned(q, 16) || !aligned(key, 16) || !aligned(value, 16) ||
+      !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(inv_freq, 8))
+    return PA_ERR_INVALID_ARG;
+  if (q_out == q && q_stride != q_row) return PA_ERR_INVALID_ARG;
+  pa::RopeParams p{};
+  p.q = static_cast<const uint16_t *>(q);
+  p.key = static_cast<const uint16_t *>(key);
+  p.value = static_cast<const uint16_t *>(value);
+  p.q_out = static_cast<uint16_t *>(q_out);
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.slots = slot_mapping;
+  p.positions = positions;
+  p.inv_freq = inv_freq;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.num_slots = static_cast<int64_t>(num_blocks) * pa::kBS;
+  p.num_tokens = num_tokens;
+  p.num_q_heads = num_q_heads;
+  p.num_kv_heads = num_kv_heads;
+  p.rotary_dim = rotary_dim;
+  p.rope_scale = rope_scale;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool il = interleaved != 0, fp8 = kv_dtype == PA_KV_FP8_E4M3;
+  if (head_dim == 128) return fp8 ? launch_rope<128, true>(p, il, st) : launch_rope<128, false>(p, il, st);
+  return fp8 ? launch_rope<64, true>(p, il, st) : launch_rope<64, false>(p, il, st);
+}
+
+pa_status pa_extend_tables(int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
+                           const int32_t *new_lens, const int32_t *free_blocks, int free_capacity,
+                           const int32_t *free_count, int32_t *context_lens_out,
+                           int32_t *free_count_out, int64_t *slot_mapping, int32_t *positions,
+                           int32_t *query_start, int num_seqs, int num_tokens, int block_size,
+                           int num_blocks, void *stream) {
+  if (num_seqs < 0 || num_tokens < 0 || max_blocks_per_seq < 0 || free_capacity < 0 || num_blocks <= 0)
+    return PA_ERR_INVALID_ARG;
+  if (block_size != pa::kBS) return PA_ERR_UNSUPPORTED;
+  if (num_seqs > pa::kTabMaxSeqs) return PA_ERR_UNSUPPORTED;
+  if (!free_count || !free_count_out || !query_start) return PA_ERR_INVALID_ARG;
+  if (free_capacity > 0 && !free_blocks) return PA_ERR_INVALID_ARG;
+  if (num_seqs > 0 && (!context_lens || !new_lens || !context_lens_out)) return PA_ERR_INVALID_ARG;
+  if (num_seqs > 0 && max_blocks_per_seq > 0 && !block_tables) return PA_ERR_INVALID_ARG;
+  if (num_tokens > 0 && (!slot_mapping || !positions)) return PA_ERR_INVALID_ARG;
+  if (!aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(new_lens, 4) ||
+      !aligned(free_blocks, 4) || !aligned(free_count, 4) || !aligned(context_lens_out, 4) ||
+      !aligned(free_count_out, 4) || !aligned(slot_mapping, 8) || !aligned(positions, 4) ||
+      !aligned(query_start, 4))
+    return PA_ERR_INVALID_ARG;
+  pa::ExtendParams p{};
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.new_lens = new_lens;
+  p.free_blocks = free_blocks;
+  p.free_count = free_count;
+  p.context_lens_out = context_lens_out;
+  p.free_count_out = free_count_out;
+  p.slot_mapping = slot_mapping;
+  p.positions = positions;
+  p.query_start = query_start;
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.num_seqs = num_seqs;
+  p.num_tokens = num_tokens;
+  p.num_blocks = num_blocks;
+  p.free_capacity = free_capacity;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  static std::atomic<uint64_t> attr_done{0};
+  const pa_status rc = launch_table_kernel(pa::extend_rows_kernel, p, num_seqs, attr_done, st);
+  if (rc != PA_OK || num_tokens == 0) return rc;
+  const int64_t per_cta = pa::kTokThreads * pa::kTokPerThread;
+  const int64_t ctas = (num_tokens + per_cta - 1) / per_cta;
+  pa::extend_tokens_kernel<<<static_cast<unsigned>(ctas), pa::kTokThreads, 0, st>>>(p);
+  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+pa_status pa_release_tables(const int32_t *block_tables, int max_blocks_per_seq,
+                            const int32_t *context_lens, const int32_t *release,
+                            int32_t *free_blocks, int free_capacity, const int32_t *free_count,
+                            int32_t *context_lens_out, int32_t *free_count_out, int keep_blocks,
+                            int num_seqs, int block_size, int num_blocks, void *stream) {
+  if (num_seqs < 0 || max_blocks_per_seq < 0 || free_capacity < 0 || keep_blocks < 0 || num_blocks <= 0)
+    return PA_ERR_INVALID_ARG;
+  if (block_size != pa::kBS) return PA_ERR_UNSUPPORTED;
+  if (num_seqs > pa::kTabMaxSeqs) return PA_ERR_UNSUPPORTED;
+  if (!free_count || !free_count_out) return PA_ERR_INVALID_ARG;
+  if (free_capacity > 0 && !free_blocks) return PA_ERR_INVALID_ARG;
+  if (num_seqs > 0 && (!context_lens || !release || !context_lens_out)) return PA_ERR_INVALID_ARG;
+  if (num_seqs > 0 && max_blocks_per_seq > 0 && !block_tables) return PA_ERR_INVALID_ARG;
+  if (!aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(release, 4) ||
+      !aligned(free_blocks, 4) || !aligned(free_count, 4) || !aligned(context_lens_out, 4) ||
+      !aligned(free_count_out, 4))
+    return PA_ERR_INVALID_ARG;
+  pa::ReleaseParams p{};
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.release = release;
+  p.free_blocks = free_blocks;
+  p.free_count = free_count;
+  p.context_lens_out = context_lens_out;
+  p.free_count_out = free_count_out;
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.num_seqs = num_seqs;
+  p.num_blocks = num_blocks;
+  p.free_capacity = free_capacity;
+  p.keep_blocks = keep_blocks;
+  static std::atomic<uint64_t> attr_done{0};
+  return launch_table_kernel(pa::release_rows_kernel, p, num_seqs, attr_done,
+                             static_cast<cudaStream_t>(stream));
 }
 
 pa_status pa_copy_blocks(void *k_cache, void *v_cache, const int64_t *block_pairs, int num_pairs,

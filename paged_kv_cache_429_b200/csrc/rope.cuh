@@ -1,0 +1,179 @@
+// Rotary positions of a step's queries and keys, with the keys and values
+// written to their cache slots in the same pass.
+//
+// The key rows that reshape_and_cache ("第 7 章推理框架：vLLM 与
+// PagedAttention" §7.1 "Block 与 Block Table"; "GPU 学习日报 Day 28" §4.2)
+// stores are already rotated; this kernel takes the projections' output
+// instead. For pair i of a head (elements (i, i + r/2), or (2i, 2i + 1)
+// interleaved, of its first r) of the token at position t:
+//     theta = t * inv_freq[i],
+//     (a, b) -> rope_scale * (a cos theta - b sin theta, b cos theta + a sin theta),
+// in fp32, rounded once to what is stored (bf16, or E4M3 of y / scale).
+//
+// The angle. t * inv_freq in fp32 is off by up to 2^-25 of the angle: 4e-3
+// radians at position 131072, more than bf16 resolves. Only the fraction of
+// a turn matters, so inv_freq / 2 pi is held as a 64-bit fixed-point
+// fraction of a turn, F = round(2^64 frac(inv_freq / 2 pi)), and
+// t * F mod 2^64 — one integer product that wraps — is the exact fraction
+// of the turn; its high word as a float (2^-25 of a half turn) goes to
+// sincospi.
+//
+// What bounds it: DRAM for prompts. Layout: a CTA takes a few tokens,
+// computes each (token, pair)'s cosine and sine once into shared memory,
+// then moves units of 16 elements (two 16-byte loads, two stores): a pair
+// of partner chunks in the half layout, two neighbouring chunks in the
+// interleaved one, so every unit needs eight consecutive frequencies.
+#pragma once
+
+#include "cache_ops.cuh"
+
+namespace pa {
+
+constexpr int kRopeThreads = 256;
+constexpr int kRopeTokens = 4;     // tokens of a CTA
+constexpr int kRopeMaxPairs = 64;  // rotary_dim <= 128
+
+struct RopeParams {
+  const uint16_t *q;          // bf16, token stride q_stride, heads contiguous
+  const uint16_t *key;
+  const uint16_t *value;
+  uint16_t *q_out;            // bf16 [T][Hq][D]
+  void *k_cache;
+  void *v_cache;
+  const int64_t *slots;       // [T]
+  const int32_t *positions;   // [T]
+  const double *inv_freq;     // [rotary_dim / 2]
+  int64_t q_stride, k_stride, v_stride;  // elements
+  int64_t num_slots;
+  int num_tokens;
+  int num_q_heads;
+  int num_kv_heads;
+  int rotary_dim;
+  float rope_scale;
+  float k_scale, v_scale;
+};
+
+// cosine and sine of position * inv_freq (see the head comment), times scale
+__device__ __forceinline__ float2 rope_cos_sin(int position, double inv_freq, float scale) {
+  double turn = inv_freq * 0.15915494309189533577;  // 1 / 2 pi
+  turn -= rint(turn);
+  const int64_t f = __double2ll_rn(turn * 18446744073709551616.0);
+  const uint64_t a = static_cast<uint64_t>(static_cast<int64_t>(position)) * static_cast<uint64_t>(f);
+  const float half_turns = static_cast<float>(static_cast<int32_t>(a >> 32)) * 4.656612873077393e-10f;
+  float s, c;
+  sincospif(half_turns, &s, &c);
+  return make_float2(c * scale, s * scale);
+}
+
+__device__ __forceinline__ void unpack8(const uint4 x, float (&f)[8]) {
+  unpack2<false>(x.x, f[0], f[1]);
+  unpack2<false>(x.y, f[2], f[3]);
+  unpack2<false>(x.z, f[4], f[5]);
+  unpack2<false>(x.w, f[6], f[7]);
+}
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  return make_uint4(pack2<false>(f[0], f[1]), pack2<false>(f[2], f[3]), pack2<false>(f[4], f[5]),
+                    pack2<false>(f[6], f[7]));
+}
+// eight floats -> E4M3(f / scale), rounded once from fp32
+__device__ __forceinline__ uint2 e4m3_of8(const float (&f)[8], float scale) {
+  uint32_t o[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(
+        make_float2(__fdiv_rn(f[4 * j], scale), __fdiv_rn(f[4 * j + 1], scale)), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(
+        make_float2(__fdiv_rn(f[4 * j + 2], scale), __fdiv_rn(f[4 * j + 3], scale)), __NV_SATFINITE, __NV_E4M3);
+    o[j] = (lo & 0xFFFFu) | (hi << 16);
+  }
+  return make_uint2(o[0], o[1]);
+}
+
+template <int D, bool FP8, bool INTERLEAVED>
+__global__ void __launch_bounds__(kRopeThreads) rope_and_cache_kernel(const RopeParams p) {
+  constexpr int UNITS = D / 16;  // units of a head row
+  __shared__ float2 s_cs[kRopeTokens][kRopeMaxPairs];
+  __shared__ int64_t s_slot[kRopeTokens];
+  const int pairs = p.rotary_dim / 2;
+  const int t0 = blockIdx.x * kRopeTokens;
+  const int nt = min(kRopeTokens, p.num_tokens - t0);
+  for (int i = threadIdx.x; i < nt * pairs; i += kRopeThreads) {
+    const int t = i / pairs, f = i - t * pairs;
+    s_cs[t][f] = rope_cos_sin(p.positions[t0 + t], p.inv_freq[f], p.rope_scale);
+  }
+  if (static_cast<int>(threadIdx.x) < nt) {
+    int64_t slot = p.slots[t0 + threadIdx.x];
+    if (slot >= p.num_slots) {
+      raise_error(kErrSlotRange);
+      slot = -1;
+    }
+    s_slot[threadIdx.x] = slot;
+  }
+  __syncthreads();
+  const int rows = p.num_q_heads + 2 * p.num_kv_heads;
+  const int per_token = rows * UNITS;
+  for (int i = threadIdx.x; i < nt * per_token; i += kRopeThreads) {
+    const int tl = i / per_token;
+    const int r = (i - tl * per_token) / UNITS;
+    const int u = i % UNITS;
+    const int64_t t = t0 + tl;
+    const bool is_q = r < p.num_q_heads;
+    const bool is_v = r >= p.num_q_heads + p.num_kv_heads;
+    const int h = is_q ? r : (is_v ? r - p.num_q_heads - p.num_kv_heads : r - p.num_q_heads);
+    const int64_t slot = s_slot[tl];
+    if (!is_q && slot < 0) continue;
+    const bool turned = !is_v && 16 * u < p.rotary_dim;
+    // the unit's two chunks of 8 elements
+    const int e0 = (turned && !INTERLEAVED) ? 8 * u : 16 * u;
+    const int e1 = (turned && !INTERLEAVED) ? p.rotary_dim / 2 + 8 * u : 16 * u + 8;
+    const uint16_t *src = is_q ? p.q + t * p.q_stride : (is_v ? p.value + t * p.v_stride : p.key + t * p.k_stride);
+    src += static_cast<int64_t>(h) * D;
+    const uint4 x0 = *reinterpret_cast<const uint4 *>(src + e0);
+    const uint4 x1 = *reinterpret_cast<const uint4 *>(src + e1);
+    float a[8], b[8];
+    unpack8(x0, a);
+    unpack8(x1, b);
+    if (turned) {
+      const float2 *cs = &s_cs[tl][8 * u];
+      if constexpr (INTERLEAVED) {
+#pragma unroll
+        for (int k = 0; k < 8; k += 2) {
+          const float2 w = cs[k / 2], z = cs[4 + k / 2];
+          const float a0 = a[k], a1 = a[k + 1], b0 = b[k], b1 = b[k + 1];
+          a[k] = a0 * w.x - a1 * w.y;
+          a[k + 1] = a1 * w.x + a0 * w.y;
+          b[k] = b0 * z.x - b1 * z.y;
+          b[k + 1] = b1 * z.x + b0 * z.y;
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float2 w = cs[k];
+          const float a0 = a[k], b0 = b[k];
+          a[k] = a0 * w.x - b0 * w.y;
+          b[k] = b0 * w.x + a0 * w.y;
+        }
+      }
+    }
+    if (is_q) {
+      uint16_t *dst = p.q_out + (t * p.num_q_heads + h) * D;
+      *reinterpret_cast<uint4 *>(dst + e0) = turned ? pack8(a) : x0;
+      *reinterpret_cast<uint4 *>(dst + e1) = turned ? pack8(b) : x1;
+    } else {
+      const int64_t row = ((slot / kBS * p.num_kv_heads + h) * kBS + slot % kBS) * D;
+      void *cache = is_v ? p.v_cache : p.k_cache;
+      if constexpr (FP8) {
+        const float scale = is_v ? p.v_scale : p.k_scale;
+        uint8_t *dst = static_cast<uint8_t *>(cache) + row;
+        *reinterpret_cast<uint2 *>(dst + e0) = e4m3_of8(a, scale);
+        *reinterpret_cast<uint2 *>(dst + e1) = e4m3_of8(b, scale);
+      } else {
+        uint16_t *dst = static_cast<uint16_t *>(cache) + row;
+        *reinterpret_cast<uint4 *>(dst + e0) = turned ? pack8(a) : x0;
+        *reinterpret_cast<uint4 *>(dst + e1) = turned ? pack8(b) : x1;
+      }
+    }
+  }
+}
+
+}  // namespace pa

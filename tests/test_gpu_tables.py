@@ -1,0 +1,349 @@
+"""GPU tests of pa_extend_tables and pa_release_tables against a row-by-row
+implementation in plain Python: whole numbers, so everything is equal."""
+import numpy as np
+import pytest
+import torch
+
+from paged_kv_cache_429_b200 import (BlockPool, pa_extend_tables, pa_get_device_error,
+                                     pa_release_tables)
+
+pytestmark = pytest.mark.gpu
+
+B = 16
+OUT_OF_BLOCKS, LENGTH, FREE, BLOCK = 0x20, 0x40, 0x80, 0x10
+
+
+@pytest.fixture(autouse=True)
+def _clean():
+    pa_get_device_error()
+    yield
+    pa_get_device_error()
+
+
+def plain_extend(tables, lens, new, free, count, T, nb):
+    """(tables, lens, count, slots, positions, query_start, flags)."""
+    tables, lens = tables.copy(), lens.astype(np.int64)
+    S, W = tables.shape
+    slots, pos = np.full(T, -1, np.int64), np.zeros(T, np.int32)
+    start = np.zeros(S + 1, np.int64)
+    need = [-(-int(a + n) // B) - -(-int(a) // B) for a, n in zip(lens, new)]
+    flags = 0
+    if S and (lens.min() < 0 or new.min() < 0 or (lens + new).max() > W * B):
+        flags |= LENGTH
+    elif int(new.sum()) > T:
+        flags |= LENGTH
+    if count < 0 or count > len(free):
+        flags |= FREE
+    if not flags and sum(need) > count:
+        flags |= OUT_OF_BLOCKS
+    if flags:
+        return tables, lens, count, slots, pos, start, flags
+    t = 0
+    for s in range(S):
+        start[s] = t
+        old = -(-int(lens[s]) // B)
+        for i in range(need[s]):
+            count -= 1
+            tables[s, old + i] = free[count]
+        for p in range(int(lens[s]), int(lens[s] + new[s])):
+            b = int(tables[s, p // B])
+            if 0 <= b < nb:
+                slots[t] = b * B + p % B
+            else:
+                flags |= BLOCK
+            pos[t] = p
+            t += 1
+    start[S] = t
+    return tables, lens + new, count, slots, pos, start, flags
+
+
+def plain_release(tables, lens, rel, free, count, keep, nb):
+    free, lens = free.copy(), lens.astype(np.int64)
+    S, W = tables.shape
+    flags = 0
+    if any(r and (a < 0 or a > W * B) for a, r in zip(lens, rel)):
+        flags |= LENGTH
+    held = 0 if flags else sum(max(-(-int(a) // B) - keep, 0) for a, r in zip(lens, rel) if r)
+    if count < 0 or count > len(free) or (not flags and count + held > len(free)):
+        flags |= FREE
+    if flags:
+        return free, lens, count, flags
+    for s in range(S):
+        if not rel[s]:
+            continue
+        for j in range(keep, -(-int(lens[s]) // B)):
+            free[count] = tables[s, j]
+            flags |= 0 if 0 <= tables[s, j] < nb else BLOCK
+            count += 1
+        lens[s] = min(int(lens[s]), keep * B)
+    return free, lens, count, flags
+
+
+def dev(a, dt=np.int32):
+    return torch.from_numpy(np.ascontiguousarray(a, dtype=dt)).cuda()
+
+
+def state(seed, S, W, max_len, nb_spare=40):
+    """Tables whose rows hold distinct blocks of a shuffled pool, and the rest as a free stack."""
+    g = np.random.default_rng(seed)
+    lens = g.integers(0, max_len + 1, S)
+    held = -(-lens // B)
+    nb = int(held.sum()) + nb_spare
+    ids = g.permutation(nb)
+    tables = np.full((S, W), -1, np.int32)
+    k = 0
+    for s in range(S):
+        tables[s, :held[s]] = ids[k:k + held[s]]
+        k += held[s]
+    free = np.concatenate([ids[k:], np.full(k, -7)]).astype(np.int32)
+    return g, tables, lens, free, nb - k, nb
+
+
+def run_extend(tables, lens, new, free, count, T, nb, inplace=False, offset=0):
+    t, ln, nw, fr, ct = dev(tables), dev(lens), dev(new), dev(free), dev([count])
+    lo = ln if inplace else torch.full_like(ln, -99)
+    co = ct if inplace else torch.full_like(ct, -99)
+    # outputs at odd offsets inside larger buffers: neighbours must stay
+    sl = torch.full((T + offset + 3,), -5, dtype=torch.int64, device="cuda")
+    ps = torch.full((T + offset + 3,), -5, dtype=torch.int32, device="cuda")
+    qs = torch.full((len(lens) + 1,), -5, dtype=torch.int32, device="cuda")
+    pa_extend_tables(t, ln, nw, fr, ct, lo, co, sl[offset:offset + T], ps[offset:offset + T], qs, num_blocks=nb)
+    torch.cuda.synchronize()
+    for x in (sl, ps):
+        assert torch.all(x[:offset] == -5) and torch.all(x[offset + T:] == -5)
+    np.testing.assert_array_equal(fr.cpu().numpy(), free)      # only read
+    if not inplace:
+        np.testing.assert_array_equal(ln.cpu().numpy(), lens)
+        assert int(ct) == count
+    return [x.cpu().numpy() for x in (t, lo, co, sl[offset:offset + T], ps[offset:offset + T], qs)]
+
+
+def check_extend(got, want):
+    t, lo, co, sl, ps, qs = got
+    tables, lens, count, slots, pos, start, flags = want
+    np.testing.assert_array_equal(t, tables)
+    np.testing.assert_array_equal(lo, lens)
+    assert int(co[0]) == count
+    np.testing.assert_array_equal(sl, slots)
+    np.testing.assert_array_equal(ps, pos)
+    np.testing.assert_array_equal(qs, start)
+    assert pa_get_device_error() == flags
+
+
+@pytest.mark.parametrize("inplace", [False, True])
+@pytest.mark.parametrize("S,W,max_len,new_hi,pad", [
+    (1, 1, 0, 16, 0),          # one empty row, one block
+    (1, 4, 15, 1, 5),          # a row whose next token may end a block
+    (3, 8, 100, 28, 1),
+    (33, 16, 200, 1, 7),       # a decode step
+    (130, 20, 150, 170, 301),  # prompts
+    (1024, 4, 40, 3, 0),       # a thread a row
+    (1025, 4, 40, 3, 0),       # and one more
+    (5000, 3, 40, 8, 13),
+    (2, 700, 20, 11000, 3),    # two long prompts
+])
+def test_extend_equals_the_plain_form(S, W, max_len, new_hi, pad, inplace):
+    for seed in range(2):
+        g, tables, lens, free, count, nb = state(seed, S, W, max_len)
+        new = np.minimum(g.integers(0, new_hi + 1, S), W * B - lens)
+        need = int((-(-(lens + new) // B) - -(-lens // B)).sum())
+        extra = np.arange(nb, nb + max(0, need - count), dtype=np.int32)
+        free = np.concatenate([free[:count], extra, free[count:]])
+        count += len(extra)
+        nb += len(extra)
+        T = int(new.sum()) + pad
+        want = plain_extend(tables, lens, new, free, count, T, nb)
+        assert want[-1] == 0
+        check_extend(run_extend(tables, lens, new, free, count, T, nb, inplace, offset=seed), want)
+
+
+def test_extend_the_most_rows():
+    S, W = 16384, 2
+    g, tables, lens, free, count, nb = state(5, S, W, 31, nb_spare=20000)
+    new = np.minimum(g.integers(0, 2, S), W * B - lens)
+    want = plain_extend(tables, lens, new, free, count, S, nb)
+    check_extend(run_extend(tables, lens, new, free, count, S, nb), want)
+
+
+def test_extend_without_rows_or_tokens():
+    got = run_extend(np.empty((0, 4), np.int32), np.empty(0, np.int64), np.empty(0, np.int64),
+                     np.arange(5, dtype=np.int32), 3, 6, 5)
+    check_extend(got, plain_extend(np.empty((0, 4), np.int32), np.empty(0, np.int64), np.empty(0, np.int64),
+                                   np.arange(5, dtype=np.int32), 3, 6, 5))
+    g, tables, lens, free, count, nb = state(1, 9, 8, 60)
+    got = run_extend(tables, lens, np.zeros(9, np.int64), free, count, 0, nb)
+    check_extend(got, plain_extend(tables, lens, np.zeros(9, np.int64), free, count, 0, nb))
+
+
+@pytest.mark.parametrize("inplace", [False, True])
+@pytest.mark.parametrize("what", ["blocks", "row", "tokens", "negative_new", "negative_len", "count_low",
+                                  "count_high", "long_len"])
+def test_extend_is_all_or_nothing(what, inplace):
+    g, tables, lens, free, count, nb = state(3, 70, 12, 100)
+    new = np.full(70, 3)
+    T = 70 * 3 + 4
+    if what == "blocks":
+        count = 2
+    elif what == "row":
+        new[41] = 12 * B - lens[41] + 1
+    elif what == "tokens":
+        T = 70 * 3 - 1
+    elif what == "negative_new":
+        new[69] = -1
+    elif what == "negative_len":
+        lens[0] = -5
+    elif what == "count_low":
+        count = -1
+    elif what == "count_high":
+        count = len(free) + 1
+    elif what == "long_len":
+        lens[7] = 2 ** 31 - 2
+    want = plain_extend(tables, lens, new, free, count, T, nb)
+    assert want[-1] != 0 and np.all(want[3] == -1)
+    check_extend(run_extend(tables, lens, new, free, count, T, nb, inplace), want)
+
+
+def test_extend_sums_past_32_bits_are_refused():
+    """Rows whose token counts add up to 2^32 + 2: a 32-bit sum would see 2."""
+    W = 2 ** 26
+    S = 5
+    lens = np.zeros(S, np.int64)
+    new = np.array([2 ** 30] * 4 + [2])
+    # the table is never touched: nothing is done
+    t = torch.zeros((S, 1), dtype=torch.int32, device="cuda")
+    from paged_kv_cache_429_b200 import _lib
+    ln, nw, fr, ct = dev(lens), dev(new), dev(np.arange(64)), dev([64])
+    sl = torch.zeros(8, dtype=torch.int64, device="cuda")
+    ps, qs = torch.ones(8, dtype=torch.int32, device="cuda"), torch.ones(S + 1, dtype=torch.int32, device="cuda")
+    rc = _lib.lib().pa_extend_tables(t.data_ptr(), W, ln.data_ptr(), nw.data_ptr(), fr.data_ptr(), 64, ct.data_ptr(),
+                                     ln.data_ptr(), ct.data_ptr(), sl.data_ptr(), ps.data_ptr(), qs.data_ptr(), S, 8,
+                                     16, 64, torch.cuda.current_stream().cuda_stream)
+    assert rc == 0
+    torch.cuda.synchronize()
+    assert int(ct) == 64 and torch.all(sl == -1) and torch.all(qs == 0) and torch.all(ln == 0)
+    assert pa_get_device_error() == LENGTH
+
+
+def test_extend_flags_ids_outside_the_pool():
+    g, tables, lens, free, count, nb = state(4, 6, 8, 90)
+    lens[:] = [5, 33, 40, 1, 16, 90]
+    new = np.full(6, 14)
+    tables[1, 2] = nb          # row 1's partly filled block
+    free[count - 1] = -3       # the first block popped
+    want = plain_extend(tables, lens, new, free, count, 90, nb)
+    assert want[-1] == BLOCK
+    check_extend(run_extend(tables, lens, new, free, count, 90, nb), want)
+
+
+@pytest.mark.parametrize("inplace", [False, True])
+@pytest.mark.parametrize("S,W,max_len,share,keep", [
+    (1, 1, 16, 1.0, 0), (1, 1, 0, 1.0, 0), (40, 20, 320, 0.3, 0), (40, 20, 320, 0.5, 4), (40, 20, 320, 1.0, 20),
+    (40, 20, 320, 0.9, 1000), (1025, 6, 96, 0.5, 1), (5000, 3, 48, 0.7, 0), (16384, 2, 32, 0.5, 0),
+    (3, 600, 9600, 1.0, 2), (0, 4, 4, 1.0, 0),
+])
+def test_release_equals_the_plain_form(S, W, max_len, share, keep, inplace):
+    g, tables, lens, free, count, nb = state(11, S, W, max_len)
+    rel = (g.random(S) < share) * g.integers(-2, 3, S)  # any non-zero value ends a row
+    fr, ln, ct, tb = dev(free), dev(lens), dev([count]), dev(tables)
+    lo = ln if inplace else torch.full_like(ln, -9)
+    co = ct if inplace else torch.full_like(ct, -9)
+    pa_release_tables(tb, ln, dev(rel), fr, ct, lo, co, keep_blocks=keep, num_blocks=nb)
+    torch.cuda.synchronize()
+    wf, wl, wc, flags = plain_release(tables, lens, rel, free, count, keep, nb)
+    assert flags == 0
+    np.testing.assert_array_equal(fr.cpu().numpy(), wf)
+    np.testing.assert_array_equal(lo.cpu().numpy(), wl)
+    assert int(co) == wc
+    np.testing.assert_array_equal(tb.cpu().numpy(), tables)
+    assert pa_get_device_error() == 0
+
+
+@pytest.mark.parametrize("what", ["full", "count_low", "count_high", "length", "bad_id"])
+def test_release_refuses_on_the_device(what):
+    g, tables, lens, free, count, nb = state(12, 20, 8, 120)
+    lens[3] = 77
+    rel = np.ones(20, np.int64)
+    if what == "full":
+        free = free[:count + 5]
+    elif what == "count_low":
+        count = -2
+    elif what == "count_high":
+        count = len(free) + 1
+    elif what == "length":
+        lens[3] = 8 * B + 1
+    elif what == "bad_id":
+        tables[3, 1] = nb + 4
+    fr, ln, ct = dev(free), dev(lens), dev([count])
+    pa_release_tables(dev(tables), ln, dev(rel), fr, ct, ln, ct, num_blocks=nb)
+    torch.cuda.synchronize()
+    wf, wl, wc, flags = plain_release(tables, lens, rel, free, count, 0, nb)
+    assert flags != 0
+    np.testing.assert_array_equal(fr.cpu().numpy(), wf)
+    np.testing.assert_array_equal(ln.cpu().numpy(), wl)
+    assert int(ct) == wc
+    assert pa_get_device_error() == flags
+
+
+def test_steps_in_a_graph_follow_the_host_pool():
+    """Decode steps captured once and replayed, rows ended and restarted
+    between replays: lengths and block counts equal a host pool's that does
+    the same, no block is held twice, and none is lost."""
+    S, W, NB = 24, 12, 260
+    pool = BlockPool(NB)
+    for s in range(S):
+        pool.add_seq(s)
+    g = np.random.default_rng(0)
+    tables = torch.full((S, W), -1, dtype=torch.int32, device="cuda")
+    lens, count = dev(np.zeros(S)), dev([NB])
+    free = dev(g.permutation(NB))
+    new, rel = dev(np.ones(S)), dev(np.zeros(S))
+    T = 3 * S
+    slots = torch.empty(T, dtype=torch.int64, device="cuda")
+    pos, qs = torch.empty(T, dtype=torch.int32, device="cuda"), torch.empty(S + 1, dtype=torch.int32, device="cuda")
+
+    def step():
+        pa_release_tables(tables, lens, rel, free, count, lens, count)
+        pa_extend_tables(tables, lens, new, free, count, lens, count, slots, pos, qs)
+
+    rel0 = rel.clone()
+    new.zero_()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()   # nothing ends, nothing comes: only warms the launches
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i in range(60):
+        n = g.integers(0, 4, S)
+        r = (g.random(S) < 0.08).astype(np.int64)
+        cur = np.array([pool.seq_len(s) for s in range(S)])
+        r[cur + 3 > W * B] = 1
+        for s in range(S):
+            if r[s]:
+                pool.free_seq(s)
+                pool.add_seq(s)
+            if n[s]:
+                pool.append(s, int(n[s]))
+        new.copy_(dev(n))
+        rel.copy_(dev(r))
+        graph.replay()
+        torch.cuda.synchronize()
+        want = np.array([pool.seq_len(s) for s in range(S)])
+        np.testing.assert_array_equal(lens.cpu().numpy(), want)
+        assert int(count) == pool.num_free
+        tb, k = tables.cpu().numpy(), int(count)
+        held = np.concatenate([tb[s, :-(-int(want[s]) // B)] for s in range(S)] + [free.cpu().numpy()[:k]])
+        assert len(np.unique(held)) == NB == len(held)
+        sl = slots.cpu().numpy()
+        total = int(n.sum())
+        assert np.all(sl[total:] == -1) and len(np.unique(sl[:total])) == total
+        at = 0
+        for s in range(S):
+            for p in range(int(want[s] - n[s]), int(want[s])):
+                assert sl[at] == tb[s, p // B] * B + p % B and int(pos[at]) == p
+                at += 1
+    assert pa_get_device_error() == 0
+    del graph
+    assert torch.count_nonzero(rel0) == 0
