@@ -22,7 +22,8 @@
  *     says "host". The library allocates no memory of its own.
  *   - GPU work is launched asynchronously on `stream` (a cudaStream_t;
  *     NULL is the legacy default stream). No call synchronises, except
- *     pa_get_device_error. pa_decode, pa_decode_append, pa_prefill,
+ *     pa_get_device_error. pa_decode, pa_decode_append,
+ *     pa_decode_shared_prefix, pa_prefill,
  *     pa_reshape_and_cache, pa_rope_and_cache, pa_extend_tables,
  *     pa_release_tables, pa_copy_blocks and pa_swap_blocks can therefore
  *     be captured in a CUDA graph and replayed; the split path's workspace
@@ -83,6 +84,10 @@ typedef enum { PA_KV_BF16 = 0, PA_KV_FP8_E4M3 = 1 } pa_kv_dtype;
                                      /* one past the table, too many tokens  */
 #define PA_DEVERR_FREE_RANGE 0x80u   /* extend, release: free count outside  */
                                      /* its array, or a push past its end    */
+#define PA_DEVERR_GROUP_RANGE 0x100u /* shared prefix: a group's prefix      */
+                                     /* outside its bound or the table       */
+                                     /* (clamped), or group_start not        */
+                                     /* ascending in [0, num_seqs]           */
 
 /* Human-readable name of a status. Never NULL; static storage. */
 PA_API const char *pa_status_string(pa_status status);
@@ -214,6 +219,56 @@ PA_API pa_status pa_decode_no_alloc(float *out, const void *q, const void *k_cac
                                     int head_dim, int block_size,
                                     int num_blocks, float sm_scale,
                                     int partition_size, void *stream);
+
+/* Bytes of workspace pa_decode_shared_prefix needs for these arguments (0
+ * for invalid ones): the partial outputs, maxima and sums of the prefixes
+ * and, where the suffixes are split, of their partitions. */
+PA_API size_t pa_decode_shared_prefix_workspace_size(int num_seqs, int num_q_heads,
+                                                     int num_kv_heads, int head_dim,
+                                                     int num_groups,
+                                                     int max_prefix_blocks,
+                                                     int max_suffix_len);
+
+/* Decode-step attention for groups of sequences that share a prefix: what
+ * pa_decode computes, with each group's prefix read and multiplied once for
+ * all its sequences ([Ch7] §7.1 前缀共享, [Day28] §4.2, §七: sharers of a
+ * system prompt hold the same physical blocks, by pa_pool_fork or the prefix
+ * cache). Group g is the sequences group_start[g] .. group_start[g + 1] - 1
+ * (neighbours in the batch); its prefix is the first prefix_blocks[g] blocks
+ * of its first sequence's table, which the group's other tables repeat
+ * (theirs are not read there). A sequence's own part starts behind them; a
+ * sequence shorter than the prefix attends to its first L tokens. Sequences
+ * of no group, and groups with a prefix of 0 blocks, attend to their whole
+ * context as their own part.
+ *   group_start    int32 [num_groups + 1], device, ascending in [0, num_seqs].
+ *   prefix_blocks  int32 [num_groups], device; max_prefix_blocks is their
+ *                  host-known bound. A value outside [0, max_prefix_blocks]
+ *                  or past the table is clamped. PA_DEVERR_GROUP_RANGE flags
+ *                  both; sequences of groups that overlap get undefined
+ *                  values (nothing faults).
+ *   max_suffix_len host-known bound of every L - 16 * prefix; longer ones are
+ *                  cut there and flagged PA_DEVERR_CONTEXT_CLAMP.
+ *   num_groups     0 up to 65535 (0: group_start and prefix_blocks are not
+ *                  read).
+ *   workspace      pa_decode_shared_prefix_workspace_size(...) bytes, 256-byte
+ *                  aligned, else PA_ERR_WORKSPACE; two calls that may run at
+ *                  the same time need one each.
+ *   Other arguments as for pa_decode; caches of both types. */
+PA_API pa_status pa_decode_shared_prefix(float *out, const void *q, const void *k_cache,
+                                         const void *v_cache, pa_kv_dtype kv_dtype,
+                                         float k_scale, float v_scale,
+                                         const int32_t *block_tables,
+                                         int max_blocks_per_seq,
+                                         const int32_t *context_lens,
+                                         int max_context_len,
+                                         const int32_t *group_start,
+                                         const int32_t *prefix_blocks, int num_groups,
+                                         int max_prefix_blocks, int max_suffix_len,
+                                         int num_seqs, int num_q_heads,
+                                         int num_kv_heads, int head_dim,
+                                         int block_size, int num_blocks,
+                                         float sm_scale, void *workspace,
+                                         size_t workspace_bytes, void *stream);
 
 /* Chunked prefill attention through block tables (bf16 caches).
  * Prefill KV is written block-wise into the same pool, and long prompts are

@@ -6,6 +6,8 @@ functions carry the names of the C entry points (include/pa.h):
 
     pa_decode               decode-step attention through block tables
     pa_decode_append        the same with the step's new tokens written to their slots in-kernel
+    pa_decode_shared_prefix  the same for groups of sequences behind shared prefixes, each prefix once
+    pa_decode_shared_prefix_workspace_size
     pa_prefill              chunked causal prefill attention through block tables
     pa_reshape_and_cache    scatter new K/V into cache slots (bf16 / fp8)
     pa_rope_and_cache       rotary positions of q and k, with the cache write in the same launch
@@ -35,6 +37,7 @@ from ._lib import STATUS_NAMES, LibraryNotBuilt
 __all__ = [
     "PA_KV_BF16", "PA_KV_FP8_E4M3", "BLOCK_SIZE", "PagedAttentionError",
     "LibraryNotBuilt", "pa_decode", "pa_decode_append", "pa_decode_no_alloc", "pa_prefill", "pa_reshape_and_cache", "pa_copy_blocks",
+    "pa_decode_shared_prefix", "pa_decode_shared_prefix_workspace_size",
     "pa_swap_blocks", "pa_rope_and_cache", "pa_rope_frequencies", "pa_extend_tables",
     "pa_release_tables", "pa_decode_workspace_size", "pa_get_device_error",
     "pa_status_string", "PA_ROPE_NONE", "PA_ROPE_LINEAR", "PA_ROPE_BASE", "PA_ROPE_BANDS",
@@ -225,6 +228,67 @@ def pa_decode_no_alloc(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor
             int(max_context_len), S, Hq, Hkv, D, B, NB, float(sm_scale),
             int(partition_size), _stream_ptr(stream, q.device))
     _ok(rc, "pa_decode_no_alloc")
+    return out
+
+
+def pa_decode_shared_prefix_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int,
+                                           head_dim: int, num_groups: int, max_prefix_blocks: int,
+                                           max_suffix_len: int) -> int:
+    return int(_lib.lib().pa_decode_shared_prefix_workspace_size(
+        num_seqs, num_q_heads, num_kv_heads, head_dim, num_groups, max_prefix_blocks,
+        max_suffix_len))
+
+
+def pa_decode_shared_prefix(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
+                            v_cache: torch.Tensor, block_tables: torch.Tensor,
+                            context_lens: torch.Tensor, max_context_len: int,
+                            group_start: torch.Tensor, prefix_blocks: torch.Tensor,
+                            max_prefix_blocks: int, sm_scale: float, *,
+                            max_suffix_len: Optional[int] = None, k_scale: float = 1.0,
+                            v_scale: float = 1.0, workspace: Optional[torch.Tensor] = None,
+                            stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Decode attention for groups of sequences behind shared prefixes (see
+    pa.h): out[S][Hq][D] fp32 is written in place. Sequences group_start[g] ..
+    group_start[g + 1] - 1 share their first prefix_blocks[g] blocks, at most
+    max_prefix_blocks of them. max_suffix_len bounds the tokens behind a
+    sequence's prefix (default: max_context_len); a tight bound keeps the
+    suffix launch small. Without a workspace one is allocated with torch for
+    this call."""
+    _need(out, "out", (torch.float32,), 3)
+    _need(q, "q", (torch.bfloat16,), 3)
+    _need(k_cache, "k_cache", (torch.bfloat16, torch.float8_e4m3fn, torch.uint8), 4)
+    _need(v_cache, "v_cache", (k_cache.dtype,), 4)
+    _need(block_tables, "block_tables", (torch.int32,), 2)
+    _need(context_lens, "context_lens", (torch.int32,), 1)
+    _need(group_start, "group_start", (torch.int32,), 1)
+    _need(prefix_blocks, "prefix_blocks", (torch.int32,), 1)
+    S, Hq, D = q.shape
+    NB, Hkv, B, Dc = k_cache.shape
+    G = prefix_blocks.shape[0]
+    if tuple(out.shape) != (S, Hq, D) or Dc != D or tuple(v_cache.shape) != tuple(k_cache.shape):
+        raise ValueError("shape mismatch between out, q and the caches")
+    if block_tables.shape[0] != S or context_lens.shape[0] != S:
+        raise ValueError("block_tables / context_lens must have num_seqs rows")
+    if group_start.shape[0] != G + 1:
+        raise ValueError("group_start must have one entry more than prefix_blocks")
+    suffix = int(max_context_len) if max_suffix_len is None else int(max_suffix_len)
+    if workspace is None:
+        nbytes = pa_decode_shared_prefix_workspace_size(S, Hq, Hkv, D, G, int(max_prefix_blocks),
+                                                        suffix)
+        if nbytes:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+    ws_ptr = workspace.data_ptr() if workspace is not None else None
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    ws = () if workspace is None else (workspace,)
+    with torch.cuda.device(_device_of(out, q, k_cache, v_cache, block_tables, context_lens,
+                                      group_start, prefix_blocks, *ws)):
+        rc = _lib.lib().pa_decode_shared_prefix(
+            out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            kv_dtype_of(k_cache), float(k_scale), float(v_scale), block_tables.data_ptr(),
+            block_tables.shape[1], context_lens.data_ptr(), int(max_context_len),
+            group_start.data_ptr(), prefix_blocks.data_ptr(), G, int(max_prefix_blocks), suffix, S,
+            Hq, Hkv, D, B, NB, float(sm_scale), ws_ptr, ws_bytes, _stream_ptr(stream, q.device))
+    _ok(rc, "pa_decode_shared_prefix")
     return out
 
 

@@ -33,6 +33,10 @@ SIGNATURES = {
     "pa_decode_no_alloc": (_i32, [_vp, _vp, _vp, _vp, _i32, _f32, _f32, _vp, _i32,
                                   _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i32,
                                   _f32, _i32, _vp]),
+    "pa_decode_shared_prefix_workspace_size": (_sz, [_i32, _i32, _i32, _i32, _i32, _i32, _i32]),
+    "pa_decode_shared_prefix": (_i32, [_vp, _vp, _vp, _vp, _i32, _f32, _f32, _vp, _i32, _vp,
+                                       _i32, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i32,
+                                       _i32, _i32, _f32, _vp, _sz, _vp]),
     "pa_prefill": (_i32, [_vp, _vp, _vp, _vp, _i32, _vp, _i32, _vp, _vp, _i32, _i32, _i32,
                           _i32, _i32, _i32, _i32, _i32, _i32, _f32, _vp]),
     "pa_reshape_and_cache": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32,

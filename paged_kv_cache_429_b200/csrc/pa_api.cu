@@ -16,6 +16,7 @@
 #include "decode_tc.cuh"
 #include "prefill.cuh"
 #include "rope.cuh"
+#include "shared_prefix.cuh"
 #include "tables.cuh"
 
 namespace {
@@ -460,6 +461,84 @@ pa_status pa_decode_append(float *out, const void *q, const void *key, const voi
                        num_kv_heads, head_dim, block_size, num_blocks, sm_scale, partition_size,
                        workspace, workspace_bytes, stream, num_seqs > 0 ? key : nullptr,
                        num_seqs > 0 ? value : nullptr);
+}
+
+size_t pa_decode_shared_prefix_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads,
+                                              int head_dim, int num_groups, int max_prefix_blocks,
+                                              int max_suffix_len) {
+  if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || num_groups < 0 ||
+      max_prefix_blocks < 0 || max_suffix_len < 0)
+    return 0;
+  return 0;
+}
+
+pa_status pa_decode_shared_prefix(float *out, const void *q, const void *k_cache,
+                                  const void *v_cache, pa_kv_dtype kv_dtype, float k_scale,
+                                  float v_scale, const int32_t *block_tables,
+                                  int max_blocks_per_seq, const int32_t *context_lens,
+                                  int max_context_len, const int32_t *group_start,
+                                  const int32_t *prefix_blocks, int num_groups,
+                                  int max_prefix_blocks, int max_suffix_len, int num_seqs,
+                                  int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                                  int num_blocks, float sm_scale, void *workspace,
+                                  size_t workspace_bytes, void *stream) {
+  if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 ||
+      max_blocks_per_seq < 0 || max_context_len < 0 || num_blocks <= 0 || num_groups < 0 ||
+      max_prefix_blocks < 0 || max_suffix_len < 0)
+    return PA_ERR_INVALID_ARG;
+  if (kv_dtype != PA_KV_BF16 && kv_dtype != PA_KV_FP8_E4M3) return PA_ERR_INVALID_ARG;
+  if (block_size != pa::kBS) return PA_ERR_UNSUPPORTED;
+  if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
+  if (num_q_heads % num_kv_heads != 0) return PA_ERR_UNSUPPORTED;
+  const int group = num_q_heads / num_kv_heads;
+  if (group > 16) return PA_ERR_UNSUPPORTED;
+  if (!std::isfinite(sm_scale)) return PA_ERR_INVALID_ARG;
+  if (kv_dtype == PA_KV_FP8_E4M3 &&
+      !(std::isfinite(k_scale) && k_scale > 0.f && std::isfinite(v_scale) && v_scale > 0.f))
+    return PA_ERR_INVALID_ARG;
+  if (num_groups > 65535) return PA_ERR_UNSUPPORTED;
+  if (num_seqs == 0) return PA_OK;
+  if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens)
+    return PA_ERR_INVALID_ARG;
+  if (num_groups > 0 && (!group_start || !prefix_blocks)) return PA_ERR_INVALID_ARG;
+  if (!aligned(out, 16) || !aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+      !aligned(group_start, 4) || !aligned(prefix_blocks, 4))
+    return PA_ERR_INVALID_ARG;
+  const int64_t rows64 = static_cast<int64_t>(num_blocks) * num_kv_heads * pa::kBS;
+  if (rows64 + pa::kBS >= INT32_MAX) return PA_ERR_UNSUPPORTED;
+  if (num_seqs > 65535 || num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;
+  pa::SharedParams p{};
+  p.out = out;
+  p.q = static_cast<const uint16_t *>(q);
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.group_start = group_start;
+  p.prefix_blocks = prefix_blocks;
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.max_context_len = max_context_len;
+  p.max_prefix_blocks = max_prefix_blocks;
+  p.max_suffix_len = max_suffix_len;
+  p.num_groups = num_groups;
+  p.num_seqs = num_seqs;
+  p.num_q_heads = num_q_heads;
+  p.num_kv_heads = num_kv_heads;
+  p.group = group;
+  p.num_blocks = num_blocks;
+  const float log2e = 1.4426950408889634f;
+  const bool fp8 = kv_dtype == PA_KV_FP8_E4M3;
+  p.score_scale = fp8 ? sm_scale * k_scale * log2e : sm_scale * log2e;
+  p.out_scale = fp8 ? v_scale : 1.f;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const unsigned ctas = static_cast<unsigned>((static_cast<int64_t>(num_seqs) * num_q_heads + 3) / 4);
+  if (head_dim == 128)
+    fp8 ? pa::shared_prefix_simple_kernel<128, true><<<ctas, 128, 0, st>>>(p)
+        : pa::shared_prefix_simple_kernel<128, false><<<ctas, 128, 0, st>>>(p);
+  else
+    fp8 ? pa::shared_prefix_simple_kernel<64, true><<<ctas, 128, 0, st>>>(p)
+        : pa::shared_prefix_simple_kernel<64, false><<<ctas, 128, 0, st>>>(p);
+  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 pa_status pa_prefill(float *out, const void *q, const void *k_cache, const void *v_cache,

@@ -171,6 +171,35 @@ def test_release_rejects_bad_arguments_on_host(kw, expect):
     assert _lib.lib().pa_release_tables(*a.values()) == expect
 
 
+@pytest.mark.parametrize("kw,expect", [
+    (dict(S=0), OK),                       # empty batch: nothing to launch
+    (dict(S=-1), INVALID),
+    (dict(G=-1), INVALID),
+    (dict(G=65536), UNSUPPORTED),
+    (dict(maxp=-1), INVALID),
+    (dict(maxs=-1), INVALID),
+    (dict(B=8), UNSUPPORTED),
+    (dict(D=96), UNSUPPORTED),
+    (dict(Hq=12, Hkv=8), UNSUPPORTED),
+    (dict(Hq=32, Hkv=1), UNSUPPORTED),
+    (dict(dtype=9), INVALID),
+    (dict(dtype=1, ks=0.0), INVALID),
+    (dict(scale=float("inf")), INVALID),
+    (dict(NB=0), INVALID),
+    (dict(gs=None), INVALID),
+    (dict(pb=None), INVALID),
+    (dict(out=FAKE + 4), INVALID),
+    (dict(q=None), INVALID),
+    (dict(cl=None), INVALID),
+])
+def test_shared_prefix_rejects_bad_arguments_on_host(kw, expect):
+    a = dict(out=FAKE, q=FAKE, k=FAKE, v=FAKE, dtype=0, ks=1.0, vs=1.0, bt=FAKE, maxb=8, cl=FAKE, maxctx=128,
+             gs=FAKE, pb=FAKE, G=1, maxp=4, maxs=64, S=2, Hq=8, Hkv=8, D=128, B=16, NB=64, scale=0.1, ws=None, wsb=0,
+             stream=None)
+    a.update(kw)
+    assert _lib.lib().pa_decode_shared_prefix(*a.values()) == expect
+
+
 def test_binding_refuses_host_tensors_and_wrong_shapes():
     S, HQ, HKV, D, NB = 2, 4, 2, 64, 8
     bf = torch.bfloat16
