@@ -215,6 +215,89 @@ size_t workspace_bytes_for(int num_seqs, int num_q_heads, int head_dim, int max_
   return static_cast<size_t>((bytes + 255) / 256 * 256);
 }
 
+// How pa_decode_shared_prefix cuts its work, from the host-known bounds alone
+// (the workspace size must not depend on the device).
+struct SharedPlan {
+  int row_tiles;      // CTAs along the rows: pairs of 128-row query tiles over all groups
+  int splits;         // parts of the longest prefix
+  int suffix_parts;   // parts of the longest suffix
+  int part_len;
+  size_t o_bytes, m_bytes, bytes;  // 0 bytes: more parts than the grid has places
+};
+
+SharedPlan shared_plan(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int num_groups,
+                       int max_prefix_blocks, int max_suffix_len) {
+  constexpr int kSms = 148;
+  SharedPlan s{};
+  const int per_cta = 2 * (pa::kSpRows / (num_q_heads / num_kv_heads));
+  const int64_t groups = std::min(num_groups, num_seqs);
+  s.row_tiles = groups > 0 && max_prefix_blocks > 0
+                    ? static_cast<int>((num_seqs + groups * (per_cta - 1)) / per_cta)
+                    : 0;
+  // Prefix parts: the number that makes waves x (key tiles of a part + 2)
+  // smallest; two tiles stand for a CTA's start and its output.
+  if (s.row_tiles > 0) {
+    const int64_t tiles = (max_prefix_blocks + pa::kSpBlocks - 1) / pa::kSpBlocks;
+    const int64_t units = static_cast<int64_t>(s.row_tiles) * num_kv_heads;
+    int64_t best = INT64_MAX;
+    for (int64_t n = 1; n <= std::min<int64_t>(tiles, 128); ++n) {
+      const int64_t per = (tiles + n - 1) / n, used = (tiles + per - 1) / per;
+      const int64_t cost = (units * used + kSms - 1) / kSms * (per + 2);
+      if (cost < best) {
+        best = cost;
+        s.splits = static_cast<int>(used);
+      }
+    }
+  }
+  // Suffix parts: about four waves of resident CTAs (3 per SM), at least 256 tokens each.
+  const int64_t units = std::max<int64_t>(static_cast<int64_t>(num_seqs) * num_kv_heads, 1);
+  const int64_t wanted = std::max<int64_t>(1, 4 * 3 * kSms / units);
+  int64_t len = (max_suffix_len + wanted - 1) / wanted;
+  len = std::max<int64_t>((len + 127) / 128 * 128, 256);
+  s.part_len = static_cast<int>(std::min<int64_t>(len, INT32_MAX / 128 * 128));
+  const int64_t parts = std::max<int64_t>((static_cast<int64_t>(max_suffix_len) + s.part_len - 1) / s.part_len, 1);
+  s.suffix_parts = static_cast<int>(parts);
+  const int64_t rows = static_cast<int64_t>(num_seqs) * num_q_heads * (s.splits + parts);
+  s.o_bytes = (static_cast<size_t>(rows) * head_dim * 4 + 255) / 256 * 256;
+  s.m_bytes = (static_cast<size_t>(rows) * 4 + 255) / 256 * 256;
+  s.bytes = s.o_bytes + 2 * s.m_bytes;
+  return s;
+}
+
+template <int D, bool FP8, int NT>
+pa_status launch_shared_suffix(const CUtensorMap &tk, const CUtensorMap &tv, const pa::SharedParams &p,
+                               cudaStream_t st, int dev) {
+  auto kern = pa::shared_suffix_kernel<D, FP8, NT>;
+  static std::atomic<uint64_t> attr_done{0};
+  const size_t smem = pa::Plan<D, FP8, NT, false>::kSmemBytes;
+  if (!ensure_smem_attr(kern, smem, attr_done, dev)) return PA_ERR_CUDA;
+  kern<<<dim3(p.suffix_parts, p.num_kv_heads, p.num_seqs), pa::kDecodeThreads, smem, st>>>(tk, tv, p);
+  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+template <int D, bool FP8>
+pa_status launch_shared(const pa::SharedParams &p, int row_tiles, const void *k_cache, const void *v_cache,
+                        int rows, cudaStream_t st, int dev) {
+  CUtensorMap tq, tk, tv;
+  if (!make_q_tmap(&tq, p.q, p.num_seqs, p.num_q_heads, D, p.group, p.tokens_per_tile) ||
+      !make_cache_tmap<D, FP8>(&tk, k_cache, rows) || !make_cache_tmap<D, FP8>(&tv, v_cache, rows))
+    return PA_ERR_CUDA;
+  if (row_tiles > 0) {
+    auto kern = pa::shared_prefix_kernel<D, FP8>;
+    static std::atomic<uint64_t> attr_done{0};
+    using PL = pa::SpPlan<D, FP8>;
+    if (!ensure_smem_attr(kern, PL::kSmemBytes, attr_done, dev)) return PA_ERR_CUDA;
+    kern<<<dim3(row_tiles, p.num_kv_heads, p.splits), PL::kThreads, PL::kSmemBytes, st>>>(tq, tk, tv, p);
+    if (cudaGetLastError() != cudaSuccess) return PA_ERR_CUDA;
+  }
+  const pa_status rc = p.group <= 8 ? launch_shared_suffix<D, FP8, 1>(tk, tv, p, st, dev)
+                                    : launch_shared_suffix<D, FP8, 2>(tk, tv, p, st, dev);
+  if (rc != PA_OK) return rc;
+  const int64_t warps = static_cast<int64_t>(p.num_seqs) * p.num_q_heads;
+  pa::shared_join_kernel<D><<<static_cast<unsigned>((warps + 7) / 8), 256, 0, st>>>(p);
+  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
 template <int D, bool FP8>
 pa_status launch_rope(const pa::RopeParams &p, bool interleaved, cudaStream_t st) {
   const int64_t ctas = (static_cast<int64_t>(p.num_tokens) + pa::kRopeTokens - 1) / pa::kRopeTokens;
@@ -467,9 +550,12 @@ size_t pa_decode_shared_prefix_workspace_size(int num_seqs, int num_q_heads, int
                                               int head_dim, int num_groups, int max_prefix_blocks,
                                               int max_suffix_len) {
   if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || num_groups < 0 ||
-      max_prefix_blocks < 0 || max_suffix_len < 0)
+      max_prefix_blocks < 0 || max_suffix_len < 0 || num_q_heads % num_kv_heads != 0 ||
+      num_q_heads / num_kv_heads > 16)
     return 0;
-  return 0;
+  return shared_plan(num_seqs, num_q_heads, num_kv_heads, head_dim, num_groups, max_prefix_blocks,
+                     max_suffix_len)
+      .bytes;
 }
 
 pa_status pa_decode_shared_prefix(float *out, const void *q, const void *k_cache,
@@ -510,8 +596,6 @@ pa_status pa_decode_shared_prefix(float *out, const void *q, const void *k_cache
   pa::SharedParams p{};
   p.out = out;
   p.q = static_cast<const uint16_t *>(q);
-  p.k_cache = k_cache;
-  p.v_cache = v_cache;
   p.block_tables = block_tables;
   p.context_lens = context_lens;
   p.group_start = group_start;
@@ -530,15 +614,27 @@ pa_status pa_decode_shared_prefix(float *out, const void *q, const void *k_cache
   const bool fp8 = kv_dtype == PA_KV_FP8_E4M3;
   p.score_scale = fp8 ? sm_scale * k_scale * log2e : sm_scale * log2e;
   p.out_scale = fp8 ? v_scale : 1.f;
+  const SharedPlan plan = shared_plan(num_seqs, num_q_heads, num_kv_heads, head_dim, num_groups,
+                                      max_prefix_blocks, max_suffix_len);
+  if (plan.bytes == 0) return PA_ERR_UNSUPPORTED;
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < plan.bytes) return PA_ERR_WORKSPACE;
+  p.tokens_per_tile = pa::kSpRows / group;
+  p.splits = plan.splits;
+  p.suffix_parts = plan.suffix_parts;
+  p.part_len = plan.part_len;
+  char *ws = static_cast<char *>(workspace);
+  p.ws_o = reinterpret_cast<float *>(ws);
+  p.ws_m = reinterpret_cast<float *>(ws + plan.o_bytes);
+  p.ws_l = reinterpret_cast<float *>(ws + plan.o_bytes + plan.m_bytes);
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return PA_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const unsigned ctas = static_cast<unsigned>((static_cast<int64_t>(num_seqs) * num_q_heads + 3) / 4);
+  const int rows = static_cast<int>(rows64);
   if (head_dim == 128)
-    fp8 ? pa::shared_prefix_simple_kernel<128, true><<<ctas, 128, 0, st>>>(p)
-        : pa::shared_prefix_simple_kernel<128, false><<<ctas, 128, 0, st>>>(p);
-  else
-    fp8 ? pa::shared_prefix_simple_kernel<64, true><<<ctas, 128, 0, st>>>(p)
-        : pa::shared_prefix_simple_kernel<64, false><<<ctas, 128, 0, st>>>(p);
-  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    return fp8 ? launch_shared<128, true>(p, plan.row_tiles, k_cache, v_cache, rows, st, dev)
+               : launch_shared<128, false>(p, plan.row_tiles, k_cache, v_cache, rows, st, dev);
+  return fp8 ? launch_shared<64, true>(p, plan.row_tiles, k_cache, v_cache, rows, st, dev)
+             : launch_shared<64, false>(p, plan.row_tiles, k_cache, v_cache, rows, st, dev);
 }
 
 pa_status pa_prefill(float *out, const void *q, const void *k_cache, const void *v_cache,

@@ -11,7 +11,7 @@ import torch
 import paged_kv_cache_429_b200 as pa
 from paged_kv_cache_429_b200 import _lib
 
-OK, INVALID, UNSUPPORTED = 0, 1, 2
+OK, INVALID, UNSUPPORTED, WORKSPACE = 0, 1, 2, 3
 FAKE = 0x100000  # aligned non-null address; never dereferenced by these calls
 
 
@@ -191,13 +191,27 @@ def test_release_rejects_bad_arguments_on_host(kw, expect):
     (dict(out=FAKE + 4), INVALID),
     (dict(q=None), INVALID),
     (dict(cl=None), INVALID),
+    (dict(ws=None), WORKSPACE),
+    (dict(wsb=255), WORKSPACE),
+    (dict(ws=FAKE + 128), WORKSPACE),      # not 256-byte aligned
 ])
 def test_shared_prefix_rejects_bad_arguments_on_host(kw, expect):
     a = dict(out=FAKE, q=FAKE, k=FAKE, v=FAKE, dtype=0, ks=1.0, vs=1.0, bt=FAKE, maxb=8, cl=FAKE, maxctx=128,
-             gs=FAKE, pb=FAKE, G=1, maxp=4, maxs=64, S=2, Hq=8, Hkv=8, D=128, B=16, NB=64, scale=0.1, ws=None, wsb=0,
+             gs=FAKE, pb=FAKE, G=1, maxp=4, maxs=64, S=2, Hq=8, Hkv=8, D=128, B=16, NB=64, scale=0.1, ws=FAKE, wsb=1 << 30,
              stream=None)
     a.update(kw)
     assert _lib.lib().pa_decode_shared_prefix(*a.values()) == expect
+
+
+def test_shared_prefix_workspace_grows_with_its_bounds():
+    f = _lib.lib().pa_decode_shared_prefix_workspace_size
+    assert f(64, 64, 8, 128, 1, 2048, 1024) > f(64, 64, 8, 128, 1, 0, 1024) > 0
+    # one part of a suffix and none of a prefix: o, then m and l, 256-byte aligned
+    assert f(256, 8, 8, 128, 0, 0, 100) == 256 * 8 * 512 + 2 * 256 * 8 * 4
+    assert f(0, 8, 8, 128, 0, 0, 100) == 0
+    assert f(4, 9, 8, 128, 1, 4, 100) == 0      # not a whole group
+    assert f(4, 8, 8, 128, 1, -1, 100) == 0
+    assert f(4, 32, 1, 128, 1, 4, 100) == 0     # a group of 32
 
 
 def test_binding_refuses_host_tensors_and_wrong_shapes():
