@@ -26,6 +26,7 @@ float8_e4m3fn (uint8 is accepted for fp8 bytes).
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional, Sequence
 
 import numpy as np
@@ -104,6 +105,48 @@ def _need(t: torch.Tensor, name: str, dtypes, ndim: int, cuda: bool = True):
         raise ValueError(f"{name} must be contiguous")
     if cuda and not t.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device")
+
+
+def _check_all(tensors, specs) -> int:
+    """_need and _device_of over a call's tensors in one pass, for the calls
+    whose launch takes a few microseconds: the index of their device. Each
+    spec is (name, dtypes, dims); whatever the pass does not like goes
+    through _need, which says what it is."""
+    try:
+        dev = tensors[0].get_device()
+        for t, (_, dtypes, ndim) in zip(tensors, specs):
+            if (t.get_device() != dev or t.dim() != ndim or t.dtype not in dtypes
+                    or not t.is_contiguous()):
+                break
+        else:
+            if dev >= 0:
+                return dev
+    except AttributeError:  # not a tensor
+        pass
+    for t, (name, dtypes, ndim) in zip(tensors, specs):
+        _need(t, name, dtypes, ndim)
+    return _device_of(*tensors).index
+
+
+def _call(what: str, dev: int, *args) -> None:
+    """One launching entry point with device `dev` current."""
+    fn = getattr(_lib.lib(), what)
+    if torch._C._cuda_getDevice() == dev:
+        rc = fn(*args)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args)
+    if rc != 0:
+        raise PagedAttentionError(rc, what)
+
+
+def _raw_stream(stream: Optional[torch.cuda.Stream], dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+_BF16, _I32, _I64, _F32, _F64 = ((torch.bfloat16,), (torch.int32,), (torch.int64,),
+                                 (torch.float32,), (torch.float64,))
+_KV = (torch.bfloat16, torch.float8_e4m3fn, torch.uint8)
 
 
 def pa_decode_workspace_size(num_seqs: int, num_q_heads: int, head_dim: int,
@@ -254,42 +297,45 @@ def pa_decode_shared_prefix(out: torch.Tensor, q: torch.Tensor, k_cache: torch.T
     sequence's prefix (default: max_context_len); a tight bound keeps the
     suffix launch small. Without a workspace one is allocated with torch for
     this call."""
-    _need(out, "out", (torch.float32,), 3)
-    _need(q, "q", (torch.bfloat16,), 3)
-    _need(k_cache, "k_cache", (torch.bfloat16, torch.float8_e4m3fn, torch.uint8), 4)
-    _need(v_cache, "v_cache", (k_cache.dtype,), 4)
-    _need(block_tables, "block_tables", (torch.int32,), 2)
-    _need(context_lens, "context_lens", (torch.int32,), 1)
-    _need(group_start, "group_start", (torch.int32,), 1)
-    _need(prefix_blocks, "prefix_blocks", (torch.int32,), 1)
+    dev = _check_all((out, q, k_cache, v_cache, block_tables, context_lens, group_start,
+                      prefix_blocks), _SHARED_SPECS)
     S, Hq, D = q.shape
     NB, Hkv, B, Dc = k_cache.shape
     G = prefix_blocks.shape[0]
-    if tuple(out.shape) != (S, Hq, D) or Dc != D or tuple(v_cache.shape) != tuple(k_cache.shape):
+    if out.shape != q.shape or Dc != D or v_cache.shape != k_cache.shape:
         raise ValueError("shape mismatch between out, q and the caches")
+    if v_cache.dtype != k_cache.dtype:
+        raise TypeError(f"v_cache: dtype {v_cache.dtype} not in {(k_cache.dtype,)}")
     if block_tables.shape[0] != S or context_lens.shape[0] != S:
         raise ValueError("block_tables / context_lens must have num_seqs rows")
     if group_start.shape[0] != G + 1:
         raise ValueError("group_start must have one entry more than prefix_blocks")
-    suffix = int(max_context_len) if max_suffix_len is None else int(max_suffix_len)
+    max_context_len, max_prefix_blocks = int(max_context_len), int(max_prefix_blocks)
+    suffix = max_context_len if max_suffix_len is None else int(max_suffix_len)
+    st = _raw_stream(stream, dev)
     if workspace is None:
-        nbytes = pa_decode_shared_prefix_workspace_size(S, Hq, Hkv, D, G, int(max_prefix_blocks),
-                                                        suffix)
-        if nbytes:
+        # allocated for the stream that uses it
+        nbytes = _shared_ws(S, Hq, Hkv, D, G, max_prefix_blocks, suffix)
+        if stream is None:
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-    ws_ptr = workspace.data_ptr() if workspace is not None else None
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    ws = () if workspace is None else (workspace,)
-    with torch.cuda.device(_device_of(out, q, k_cache, v_cache, block_tables, context_lens,
-                                      group_start, prefix_blocks, *ws)):
-        rc = _lib.lib().pa_decode_shared_prefix(
-            out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-            kv_dtype_of(k_cache), float(k_scale), float(v_scale), block_tables.data_ptr(),
-            block_tables.shape[1], context_lens.data_ptr(), int(max_context_len),
-            group_start.data_ptr(), prefix_blocks.data_ptr(), G, int(max_prefix_blocks), suffix, S,
-            Hq, Hkv, D, B, NB, float(sm_scale), ws_ptr, ws_bytes, _stream_ptr(stream, q.device))
-    _ok(rc, "pa_decode_shared_prefix")
+        else:
+            with torch.cuda.stream(stream):
+                workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+    elif workspace.get_device() != dev:
+        raise ValueError("the workspace must be on the device of the call's tensors")
+    _call("pa_decode_shared_prefix", dev,
+          out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+          kv_dtype_of(k_cache), k_scale, v_scale, block_tables.data_ptr(), block_tables.shape[1],
+          context_lens.data_ptr(), max_context_len, group_start.data_ptr(), prefix_blocks.data_ptr(),
+          G, max_prefix_blocks, suffix, S, Hq, Hkv, D, B, NB, sm_scale, workspace.data_ptr(),
+          workspace.numel() * workspace.element_size(), st)
     return out
+
+
+_SHARED_SPECS = (("out", _F32, 3), ("q", _BF16, 3), ("k_cache", _KV, 4), ("v_cache", _KV, 4),
+                 ("block_tables", _I32, 2), ("context_lens", _I32, 1), ("group_start", _I32, 1),
+                 ("prefix_blocks", _I32, 1))
+_shared_ws = functools.lru_cache(maxsize=256)(pa_decode_shared_prefix_workspace_size)
 
 
 def pa_prefill(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
@@ -362,6 +408,13 @@ def pa_rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: int = P
 def _need_rows(t: torch.Tensor, name: str):
     """bf16 [tokens][heads][head_dim] with each token's heads contiguous; any
     token stride (a view of a fused projection)."""
+    try:
+        if t.dtype is torch.bfloat16 and t.is_cuda:
+            (_, heads, dim), (_, hs, ds) = t.shape, t.stride()
+            if ds == 1 and (hs == dim or heads == 1):
+                return
+    except (AttributeError, ValueError):  # not a tensor, or not of three dims
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != torch.bfloat16:
@@ -390,33 +443,32 @@ def pa_rope_and_cache(q_out: torch.Tensor, q: torch.Tensor, key: torch.Tensor,
     their slots of the caches. q, key, value may be views with a token
     stride; the rotated part of a head is its first 2 * len(inv_freq)
     elements."""
-    _need(q_out, "q_out", (torch.bfloat16,), 3)
-    _need_rows(q, "q")
-    _need_rows(key, "key")
-    _need_rows(value, "value")
-    _need(k_cache, "k_cache", (torch.bfloat16, torch.float8_e4m3fn, torch.uint8), 4)
-    _need(v_cache, "v_cache", (k_cache.dtype,), 4)
-    _need(slot_mapping, "slot_mapping", (torch.int64,), 1)
-    _need(positions, "positions", (torch.int32,), 1)
-    _need(inv_freq, "inv_freq", (torch.float64,), 1)
+    for t, name in ((q, "q"), (key, "key"), (value, "value")):
+        _need_rows(t, name)
+    dev = _check_all((q_out, k_cache, v_cache, slot_mapping, positions, inv_freq), _ROPE_SPECS)
     T, Hq, D = q.shape
     NB, Hkv, B, Dc = k_cache.shape
-    if tuple(q_out.shape) != (T, Hq, D) or Dc != D or tuple(v_cache.shape) != tuple(k_cache.shape):
+    if q_out.shape != q.shape or Dc != D or v_cache.shape != k_cache.shape:
         raise ValueError("shape mismatch between q_out, q and the caches")
-    if tuple(key.shape) != (T, Hkv, D) or tuple(value.shape) != (T, Hkv, D):
+    if v_cache.dtype != k_cache.dtype:
+        raise TypeError(f"v_cache: dtype {v_cache.dtype} not in {(k_cache.dtype,)}")
+    if key.shape != (T, Hkv, D) or value.shape != (T, Hkv, D):
         raise ValueError("key / value must be [num_tokens][num_kv_heads][head_dim]")
     if slot_mapping.shape[0] != T or positions.shape[0] != T:
         raise ValueError("slot_mapping / positions must have num_tokens entries")
-    with torch.cuda.device(_device_of(q_out, q, key, value, k_cache, v_cache, slot_mapping,
-                                      positions, inv_freq)):
-        rc = _lib.lib().pa_rope_and_cache(
-            q_out.data_ptr(), q.data_ptr(), key.data_ptr(), value.data_ptr(), k_cache.data_ptr(),
-            v_cache.data_ptr(), slot_mapping.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(),
-            2 * inv_freq.shape[0], int(bool(interleaved)), float(rope_scale), _row_stride(q),
-            _row_stride(key), _row_stride(value), T, Hq, Hkv, D, B, NB, kv_dtype_of(k_cache),
-            float(k_scale), float(v_scale), _stream_ptr(stream, q.device))
-    _ok(rc, "pa_rope_and_cache")
+    if not (q.get_device() == key.get_device() == value.get_device() == dev):
+        _device_of(q_out, q, key, value)  # says which
+    _call("pa_rope_and_cache", dev,
+          q_out.data_ptr(), q.data_ptr(), key.data_ptr(), value.data_ptr(), k_cache.data_ptr(),
+          v_cache.data_ptr(), slot_mapping.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(),
+          2 * inv_freq.shape[0], 1 if interleaved else 0, rope_scale, _row_stride(q),
+          _row_stride(key), _row_stride(value), T, Hq, Hkv, D, B, NB, kv_dtype_of(k_cache),
+          k_scale, v_scale, _raw_stream(stream, dev))
     return q_out
+
+
+_ROPE_SPECS = (("q_out", _BF16, 3), ("k_cache", _KV, 4), ("v_cache", _KV, 4),
+               ("slot_mapping", _I64, 1), ("positions", _I32, 1), ("inv_freq", _F64, 1))
 
 
 def pa_extend_tables(block_tables: torch.Tensor, context_lens: torch.Tensor,
@@ -430,16 +482,9 @@ def pa_extend_tables(block_tables: torch.Tensor, context_lens: torch.Tensor,
     stack into block_tables [S][W], the new lengths and count (in place if
     the same tensors are given), slots, positions and query_start of the
     tokens. num_blocks: the pool's size (default: free_blocks' length)."""
-    _need(block_tables, "block_tables", (torch.int32,), 2)
-    _need(context_lens, "context_lens", (torch.int32,), 1)
-    _need(new_lens, "new_lens", (torch.int32,), 1)
-    _need(free_blocks, "free_blocks", (torch.int32,), 1)
-    _need(free_count, "free_count", (torch.int32,), 1)
-    _need(context_lens_out, "context_lens_out", (torch.int32,), 1)
-    _need(free_count_out, "free_count_out", (torch.int32,), 1)
-    _need(slot_mapping, "slot_mapping", (torch.int64,), 1)
-    _need(positions, "positions", (torch.int32,), 1)
-    _need(query_start, "query_start", (torch.int32,), 1)
+    dev = _check_all((block_tables, context_lens, new_lens, free_blocks, free_count,
+                      context_lens_out, free_count_out, slot_mapping, positions, query_start),
+                     _EXTEND_SPECS)
     S, W = block_tables.shape
     T = slot_mapping.shape[0]
     if context_lens.shape[0] != S or new_lens.shape[0] != S or context_lens_out.shape[0] != S:
@@ -448,17 +493,19 @@ def pa_extend_tables(block_tables: torch.Tensor, context_lens: torch.Tensor,
         raise ValueError("free_count must have one element")
     if positions.shape[0] != T or query_start.shape[0] != S + 1:
         raise ValueError("positions must have num_tokens entries, query_start num_seqs + 1")
-    nb = free_blocks.shape[0] if num_blocks is None else int(num_blocks)
-    with torch.cuda.device(_device_of(block_tables, context_lens, new_lens, free_blocks, free_count,
-                                      context_lens_out, free_count_out, slot_mapping, positions,
-                                      query_start)):
-        rc = _lib.lib().pa_extend_tables(
-            block_tables.data_ptr(), W, context_lens.data_ptr(), new_lens.data_ptr(),
-            free_blocks.data_ptr(), free_blocks.shape[0], free_count.data_ptr(),
-            context_lens_out.data_ptr(), free_count_out.data_ptr(), slot_mapping.data_ptr(),
-            positions.data_ptr(), query_start.data_ptr(), S, T, BLOCK_SIZE, nb,
-            _stream_ptr(stream, block_tables.device))
-    _ok(rc, "pa_extend_tables")
+    capacity = free_blocks.shape[0]
+    _call("pa_extend_tables", dev,
+          block_tables.data_ptr(), W, context_lens.data_ptr(), new_lens.data_ptr(),
+          free_blocks.data_ptr(), capacity, free_count.data_ptr(), context_lens_out.data_ptr(),
+          free_count_out.data_ptr(), slot_mapping.data_ptr(), positions.data_ptr(),
+          query_start.data_ptr(), S, T, BLOCK_SIZE, capacity if num_blocks is None else int(num_blocks),
+          _raw_stream(stream, dev))
+
+
+_EXTEND_SPECS = (("block_tables", _I32, 2), ("context_lens", _I32, 1), ("new_lens", _I32, 1),
+                 ("free_blocks", _I32, 1), ("free_count", _I32, 1), ("context_lens_out", _I32, 1),
+                 ("free_count_out", _I32, 1), ("slot_mapping", _I64, 1), ("positions", _I32, 1),
+                 ("query_start", _I32, 1))
 
 
 def pa_release_tables(block_tables: torch.Tensor, context_lens: torch.Tensor,
@@ -470,27 +517,24 @@ def pa_release_tables(block_tables: torch.Tensor, context_lens: torch.Tensor,
     """Push the blocks of the rows with release != 0, behind their first
     keep_blocks, on the free stack (see pa.h); lengths and count as for
     pa_extend_tables."""
-    _need(block_tables, "block_tables", (torch.int32,), 2)
-    _need(context_lens, "context_lens", (torch.int32,), 1)
-    _need(release, "release", (torch.int32,), 1)
-    _need(free_blocks, "free_blocks", (torch.int32,), 1)
-    _need(free_count, "free_count", (torch.int32,), 1)
-    _need(context_lens_out, "context_lens_out", (torch.int32,), 1)
-    _need(free_count_out, "free_count_out", (torch.int32,), 1)
+    dev = _check_all((block_tables, context_lens, release, free_blocks, free_count,
+                      context_lens_out, free_count_out), _RELEASE_SPECS)
     S, W = block_tables.shape
     if context_lens.shape[0] != S or release.shape[0] != S or context_lens_out.shape[0] != S:
         raise ValueError("context_lens / release must have num_seqs rows")
     if free_count.shape[0] != 1 or free_count_out.shape[0] != 1:
         raise ValueError("free_count must have one element")
-    nb = free_blocks.shape[0] if num_blocks is None else int(num_blocks)
-    with torch.cuda.device(_device_of(block_tables, context_lens, release, free_blocks, free_count,
-                                      context_lens_out, free_count_out)):
-        rc = _lib.lib().pa_release_tables(
-            block_tables.data_ptr(), W, context_lens.data_ptr(), release.data_ptr(),
-            free_blocks.data_ptr(), free_blocks.shape[0], free_count.data_ptr(),
-            context_lens_out.data_ptr(), free_count_out.data_ptr(), int(keep_blocks), S, BLOCK_SIZE,
-            nb, _stream_ptr(stream, block_tables.device))
-    _ok(rc, "pa_release_tables")
+    capacity = free_blocks.shape[0]
+    _call("pa_release_tables", dev,
+          block_tables.data_ptr(), W, context_lens.data_ptr(), release.data_ptr(),
+          free_blocks.data_ptr(), capacity, free_count.data_ptr(), context_lens_out.data_ptr(),
+          free_count_out.data_ptr(), int(keep_blocks), S, BLOCK_SIZE,
+          capacity if num_blocks is None else int(num_blocks), _raw_stream(stream, dev))
+
+
+_RELEASE_SPECS = (("block_tables", _I32, 2), ("context_lens", _I32, 1), ("release", _I32, 1),
+                  ("free_blocks", _I32, 1), ("free_count", _I32, 1), ("context_lens_out", _I32, 1),
+                  ("free_count_out", _I32, 1))
 
 
 def pa_copy_blocks(k_cache: torch.Tensor, v_cache: torch.Tensor,

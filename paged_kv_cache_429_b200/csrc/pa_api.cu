@@ -299,34 +299,32 @@ pa_status launch_shared(const pa::SharedParams &p, int row_tiles, const void *k_
 }
 
 template <int D, bool FP8>
-pa_status launch_rope(const pa::RopeParams &p, bool interleaved, cudaStream_t st) {
-  const int64_t ctas = (static_cast<int64_t>(p.num_tokens) + pa::kRopeTokens - 1) / pa::kRopeTokens;
+pa_status launch_rope(pa::RopeParams p, bool interleaved, cudaStream_t st, int dev) {
+  // Few tokens: one a CTA and its units cut into slices of one a thread, so
+  // that a decode step fills the GPU; from four tokens an SM on, a CTA takes
+  // four tokens whole and their angles are formed once.
+  const bool few = p.num_tokens < 4 * device_sm_count(dev);
+  p.tokens_per_cta = few ? 1 : pa::kRopeTokens;
+  const int units = p.tokens_per_cta * (p.num_q_heads + 2 * p.num_kv_heads) * (D / 16);
+  p.units_per_cta = few ? pa::kRopeThreads : units;
+  const int64_t ctas = (static_cast<int64_t>(p.num_tokens) + p.tokens_per_cta - 1) / p.tokens_per_cta;
+  const dim3 grid(static_cast<unsigned>(ctas), (units + p.units_per_cta - 1) / p.units_per_cta);
+  if (grid.y > 65535) return PA_ERR_UNSUPPORTED;
   if (interleaved)
-    pa::rope_and_cache_kernel<D, FP8, true><<<static_cast<unsigned>(ctas), pa::kRopeThreads, 0, st>>>(p);
+    pa::rope_and_cache_kernel<D, FP8, true><<<grid, pa::kRopeThreads, 0, st>>>(p);
   else
-    pa::rope_and_cache_kernel<D, FP8, false><<<static_cast<unsigned>(ctas), pa::kRopeThreads, 0, st>>>(p);
+    pa::rope_and_cache_kernel<D, FP8, false><<<grid, pa::kRopeThreads, 0, st>>>(p);
   return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
-// One cluster of pa::kTabCluster CTAs, the rows' sums in dynamic shared memory.
+// One phase of a table kernel over `ctas` CTAs, with `ints` integers of
+// dynamic shared memory (at most max_ints for any call).
 template <typename Params>
-pa_status launch_table_kernel(void (*kern)(Params), const Params &p, int num_seqs,
-                                     std::atomic<uint64_t> &attr_done, cudaStream_t st) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return PA_ERR_CUDA;
-  if (!ensure_smem_attr(kern, (pa::kTabMaxSeqs + 1) * sizeof(int32_t), attr_done, dev)) return PA_ERR_CUDA;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(pa::kTabCluster);
-  cfg.blockDim = dim3(pa::kTabThreads);
-  cfg.dynamicSmemBytes = (static_cast<size_t>(num_seqs) + 1) * sizeof(int32_t);
-  cfg.stream = st;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = pa::kTabCluster;
-  at.val.clusterDim.y = at.val.clusterDim.z = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+pa_status launch_table_kernel(void (*kern)(Params), const Params &p, int64_t ctas, size_t ints, size_t max_ints,
+                              std::atomic<uint64_t> &attr_done, cudaStream_t st, int dev) {
+  if (!ensure_smem_attr(kern, max_ints * sizeof(int32_t), attr_done, dev)) return PA_ERR_CUDA;
+  kern<<<static_cast<unsigned>(ctas), pa::kTabThreads, ints * sizeof(int32_t), st>>>(p);
+  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 }  // namespace
@@ -842,8 +840,11 @@ pa_status pa_rope_and_cache(void *q_out, const void *q, const void *key, const v
   p.v_scale = v_scale;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool il = interleaved != 0, fp8 = kv_dtype == PA_KV_FP8_E4M3;
-  if (head_dim == 128) return fp8 ? launch_rope<128, true>(p, il, st) : launch_rope<128, false>(p, il, st);
-  return fp8 ? launch_rope<64, true>(p, il, st) : launch_rope<64, false>(p, il, st);
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return PA_ERR_CUDA;
+  if (head_dim == 128)
+    return fp8 ? launch_rope<128, true>(p, il, st, dev) : launch_rope<128, false>(p, il, st, dev);
+  return fp8 ? launch_rope<64, true>(p, il, st, dev) : launch_rope<64, false>(p, il, st, dev);
 }
 
 pa_status pa_extend_tables(int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
@@ -883,13 +884,20 @@ pa_status pa_extend_tables(int32_t *block_tables, int max_blocks_per_seq, const 
   p.num_blocks = num_blocks;
   p.free_capacity = free_capacity;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  static std::atomic<uint64_t> attr_done{0};
-  const pa_status rc = launch_table_kernel(pa::extend_rows_kernel, p, num_seqs, attr_done, st);
-  if (rc != PA_OK || num_tokens == 0) return rc;
-  const int64_t per_cta = pa::kTokThreads * pa::kTokPerThread;
-  const int64_t ctas = (num_tokens + per_cta - 1) / per_cta;
-  pa::extend_tokens_kernel<<<static_cast<unsigned>(ctas), pa::kTokThreads, 0, st>>>(p);
-  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  p.wide = aligned(slot_mapping, 16) && aligned(positions, 16);
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return PA_ERR_CUDA;
+  using pa::TablePhase;
+  const size_t ints = 3 * static_cast<size_t>(num_seqs) + 1, most = 3 * pa::kTabMaxSeqs + 1;
+  static std::atomic<uint64_t> attr_all{0}, attr_work{0}, attr_finish{0};
+  if (num_tokens <= pa::kTabSmallTokens)
+    return launch_table_kernel(pa::extend_kernel<TablePhase::kAll>, p, 1, ints, most, attr_all, st, dev);
+  const int64_t ctas = std::min<int64_t>((static_cast<int64_t>(num_tokens) + pa::kTabPerCta - 1) / pa::kTabPerCta,
+                                         device_sm_count(dev));
+  const pa_status rc =
+      launch_table_kernel(pa::extend_kernel<TablePhase::kWork>, p, ctas, ints, most, attr_work, st, dev);
+  if (rc != PA_OK) return rc;
+  return launch_table_kernel(pa::extend_kernel<TablePhase::kFinish>, p, 1, 0, most, attr_finish, st, dev);
 }
 
 pa_status pa_release_tables(const int32_t *block_tables, int max_blocks_per_seq,
@@ -922,9 +930,19 @@ pa_status pa_release_tables(const int32_t *block_tables, int max_blocks_per_seq,
   p.num_blocks = num_blocks;
   p.free_capacity = free_capacity;
   p.keep_blocks = keep_blocks;
-  static std::atomic<uint64_t> attr_done{0};
-  return launch_table_kernel(pa::release_rows_kernel, p, num_seqs, attr_done,
-                             static_cast<cudaStream_t>(stream));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return PA_ERR_CUDA;
+  using pa::TablePhase;
+  static std::atomic<uint64_t> attr_all{0}, attr_work{0}, attr_finish{0};
+  const int64_t pushes = static_cast<int64_t>(num_seqs) * std::max(max_blocks_per_seq - keep_blocks, 0);  // at most
+  if (pushes <= pa::kTabSmallBlocks)
+    return launch_table_kernel(pa::release_kernel<TablePhase::kAll>, p, 1, num_seqs, pa::kTabMaxSeqs, attr_all, st, dev);
+  const int64_t ctas = std::min<int64_t>((pushes + pa::kTabPerCta - 1) / pa::kTabPerCta, device_sm_count(dev));
+  const pa_status rc = launch_table_kernel(pa::release_kernel<TablePhase::kWork>, p, ctas, num_seqs, pa::kTabMaxSeqs,
+                                           attr_work, st, dev);
+  if (rc != PA_OK) return rc;
+  return launch_table_kernel(pa::release_kernel<TablePhase::kFinish>, p, 1, 0, pa::kTabMaxSeqs, attr_finish, st, dev);
 }
 
 pa_status pa_copy_blocks(void *k_cache, void *v_cache, const int64_t *block_pairs, int num_pairs,

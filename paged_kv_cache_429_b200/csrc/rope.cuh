@@ -30,7 +30,8 @@
 namespace pa {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeTokens = 4;     // tokens of a CTA
+constexpr int kRopeTokens = 4;     // most tokens of a CTA
+constexpr int kRopeBatch = 2;      // units of a thread in flight
 constexpr int kRopeMaxPairs = 64;  // rotary_dim <= 128
 
 struct RopeParams {
@@ -46,6 +47,8 @@ struct RopeParams {
   int64_t q_stride, k_stride, v_stride;  // elements
   int64_t num_slots;
   int num_tokens;
+  int tokens_per_cta;         // <= kRopeTokens
+  int units_per_cta;          // grid.y slices of the tokens' units
   int num_q_heads;
   int num_kv_heads;
   int rotary_dim;
@@ -92,85 +95,117 @@ __device__ __forceinline__ uint2 e4m3_of8(const float (&f)[8], float scale) {
 template <int D, bool FP8, bool INTERLEAVED>
 __global__ void __launch_bounds__(kRopeThreads) rope_and_cache_kernel(const RopeParams p) {
   constexpr int UNITS = D / 16;  // units of a head row
+  constexpr int U = kRopeBatch;
   __shared__ float2 s_cs[kRopeTokens][kRopeMaxPairs];
   __shared__ int64_t s_slot[kRopeTokens];
   const int pairs = p.rotary_dim / 2;
-  const int t0 = blockIdx.x * kRopeTokens;
-  const int nt = min(kRopeTokens, p.num_tokens - t0);
-  for (int i = threadIdx.x; i < nt * pairs; i += kRopeThreads) {
-    const int t = i / pairs, f = i - t * pairs;
-    s_cs[t][f] = rope_cos_sin(p.positions[t0 + t], p.inv_freq[f], p.rope_scale);
-  }
-  if (static_cast<int>(threadIdx.x) < nt) {
-    int64_t slot = p.slots[t0 + threadIdx.x];
-    if (slot >= p.num_slots) {
-      raise_error(kErrSlotRange);
-      slot = -1;
-    }
-    s_slot[threadIdx.x] = slot;
-  }
-  __syncthreads();
-  const int rows = p.num_q_heads + 2 * p.num_kv_heads;
-  const int per_token = rows * UNITS;
-  for (int i = threadIdx.x; i < nt * per_token; i += kRopeThreads) {
-    const int tl = i / per_token;
-    const int r = (i - tl * per_token) / UNITS;
-    const int u = i % UNITS;
-    const int64_t t = t0 + tl;
-    const bool is_q = r < p.num_q_heads;
-    const bool is_v = r >= p.num_q_heads + p.num_kv_heads;
-    const int h = is_q ? r : (is_v ? r - p.num_q_heads - p.num_kv_heads : r - p.num_q_heads);
-    const int64_t slot = s_slot[tl];
-    if (!is_q && slot < 0) continue;
-    const bool turned = !is_v && 16 * u < p.rotary_dim;
-    // the unit's two chunks of 8 elements
-    const int e0 = (turned && !INTERLEAVED) ? 8 * u : 16 * u;
-    const int e1 = (turned && !INTERLEAVED) ? p.rotary_dim / 2 + 8 * u : 16 * u + 8;
-    const uint16_t *src = is_q ? p.q + t * p.q_stride : (is_v ? p.value + t * p.v_stride : p.key + t * p.k_stride);
-    src += static_cast<int64_t>(h) * D;
-    const uint4 x0 = *reinterpret_cast<const uint4 *>(src + e0);
-    const uint4 x1 = *reinterpret_cast<const uint4 *>(src + e1);
-    float a[8], b[8];
-    unpack8(x0, a);
-    unpack8(x1, b);
-    if (turned) {
-      const float2 *cs = &s_cs[tl][8 * u];
-      if constexpr (INTERLEAVED) {
+  const int t0 = blockIdx.x * p.tokens_per_cta;
+  const int nt = min(p.tokens_per_cta, p.num_tokens - t0);
+  const int per_token = (p.num_q_heads + 2 * p.num_kv_heads) * UNITS;
+  // this CTA's slice of its tokens' units
+  const int first = blockIdx.y * p.units_per_cta, last = min(first + p.units_per_cta, nt * per_token);
+
+  struct Unit {
+    const uint16_t *src;
+    int tl, h, e0, e1;
+    bool is_q, is_v, turned;
+  };
+  auto unit = [&](int i) {
+    Unit n;
+    n.tl = 0;
 #pragma unroll
-        for (int k = 0; k < 8; k += 2) {
-          const float2 w = cs[k / 2], z = cs[4 + k / 2];
-          const float a0 = a[k], a1 = a[k + 1], b0 = b[k], b1 = b[k + 1];
-          a[k] = a0 * w.x - a1 * w.y;
-          a[k + 1] = a1 * w.x + a0 * w.y;
-          b[k] = b0 * z.x - b1 * z.y;
-          b[k + 1] = b1 * z.x + b0 * z.y;
-        }
-      } else {
+    for (int k = 1; k < kRopeTokens; ++k) n.tl += i >= k * per_token;
+    const int r = (i - n.tl * per_token) / UNITS, u = i % UNITS;
+    n.is_q = r < p.num_q_heads;
+    n.is_v = r >= p.num_q_heads + p.num_kv_heads;
+    n.h = n.is_q ? r : (n.is_v ? r - p.num_q_heads - p.num_kv_heads : r - p.num_q_heads);
+    n.turned = !n.is_v && 16 * u < p.rotary_dim;
+    const bool apart = n.turned && !INTERLEAVED;
+    n.e0 = apart ? 8 * u : 16 * u;
+    n.e1 = apart ? p.rotary_dim / 2 + 8 * u : 16 * u + 8;
+    const int64_t t = t0 + n.tl;
+    n.src = (n.is_q ? p.q + t * p.q_stride : (n.is_v ? p.value + t * p.v_stride : p.key + t * p.k_stride)) + n.h * D;
+    return n;
+  };
+
+  bool ready = false;
+  for (int base = first; base < last; base += U * kRopeThreads) {
+    // the batch's loads first: they are in flight while the angles are formed
+    uint4 x0[U], x1[U];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float2 w = cs[k];
-          const float a0 = a[k], b0 = b[k];
-          a[k] = a0 * w.x - b0 * w.y;
-          b[k] = b0 * w.x + a0 * w.y;
-        }
+    for (int k = 0; k < U; ++k) {
+      const int i = base + k * kRopeThreads + threadIdx.x;
+      if (i < last) {
+        const Unit n = unit(i);
+        x0[k] = *reinterpret_cast<const uint4 *>(n.src + n.e0);
+        x1[k] = *reinterpret_cast<const uint4 *>(n.src + n.e1);
       }
     }
-    if (is_q) {
-      uint16_t *dst = p.q_out + (t * p.num_q_heads + h) * D;
-      *reinterpret_cast<uint4 *>(dst + e0) = turned ? pack8(a) : x0;
-      *reinterpret_cast<uint4 *>(dst + e1) = turned ? pack8(b) : x1;
-    } else {
-      const int64_t row = ((slot / kBS * p.num_kv_heads + h) * kBS + slot % kBS) * D;
-      void *cache = is_v ? p.v_cache : p.k_cache;
-      if constexpr (FP8) {
-        const float scale = is_v ? p.v_scale : p.k_scale;
-        uint8_t *dst = static_cast<uint8_t *>(cache) + row;
-        *reinterpret_cast<uint2 *>(dst + e0) = e4m3_of8(a, scale);
-        *reinterpret_cast<uint2 *>(dst + e1) = e4m3_of8(b, scale);
+    if (!ready) {
+      for (int i = threadIdx.x; i < nt * pairs; i += kRopeThreads) {
+        const int t = i / pairs, f = i - t * pairs;
+        s_cs[t][f] = rope_cos_sin(p.positions[t0 + t], p.inv_freq[f], p.rope_scale);
+      }
+      if (static_cast<int>(threadIdx.x) < nt) {
+        int64_t slot = p.slots[t0 + threadIdx.x];
+        if (slot >= p.num_slots) {
+          if (blockIdx.y == 0) raise_error(kErrSlotRange);
+          slot = -1;
+        }
+        s_slot[threadIdx.x] = slot;
+      }
+      __syncthreads();
+      ready = true;
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int i = base + k * kRopeThreads + threadIdx.x;
+      if (i >= last) continue;
+      const Unit n = unit(i);
+      const int64_t slot = s_slot[n.tl];
+      if (!n.is_q && slot < 0) continue;
+      float a[8], b[8];
+      unpack8(x0[k], a);
+      unpack8(x1[k], b);
+      if (n.turned) {
+        const float2 *cs = &s_cs[n.tl][8 * (i % UNITS)];
+        if constexpr (INTERLEAVED) {
+#pragma unroll
+          for (int j = 0; j < 8; j += 2) {
+            const float2 w = cs[j / 2], z = cs[4 + j / 2];
+            const float a0 = a[j], a1 = a[j + 1], b0 = b[j], b1 = b[j + 1];
+            a[j] = a0 * w.x - a1 * w.y;
+            a[j + 1] = a1 * w.x + a0 * w.y;
+            b[j] = b0 * z.x - b1 * z.y;
+            b[j + 1] = b1 * z.x + b0 * z.y;
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float2 w = cs[j];
+            const float a0 = a[j], b0 = b[j];
+            a[j] = a0 * w.x - b0 * w.y;
+            b[j] = b0 * w.x + a0 * w.y;
+          }
+        }
+      }
+      if (n.is_q) {
+        uint16_t *dst = p.q_out + (static_cast<int64_t>(t0 + n.tl) * p.num_q_heads + n.h) * D;
+        *reinterpret_cast<uint4 *>(dst + n.e0) = n.turned ? pack8(a) : x0[k];
+        *reinterpret_cast<uint4 *>(dst + n.e1) = n.turned ? pack8(b) : x1[k];
       } else {
-        uint16_t *dst = static_cast<uint16_t *>(cache) + row;
-        *reinterpret_cast<uint4 *>(dst + e0) = turned ? pack8(a) : x0;
-        *reinterpret_cast<uint4 *>(dst + e1) = turned ? pack8(b) : x1;
+        const int64_t row = ((slot / kBS * p.num_kv_heads + n.h) * kBS + slot % kBS) * D;
+        void *cache = n.is_v ? p.v_cache : p.k_cache;
+        if constexpr (FP8) {
+          const float scale = n.is_v ? p.v_scale : p.k_scale;
+          uint8_t *dst = static_cast<uint8_t *>(cache) + row;
+          *reinterpret_cast<uint2 *>(dst + n.e0) = e4m3_of8(a, scale);
+          *reinterpret_cast<uint2 *>(dst + n.e1) = e4m3_of8(b, scale);
+        } else {
+          uint16_t *dst = static_cast<uint16_t *>(cache) + row;
+          *reinterpret_cast<uint4 *>(dst + n.e0) = n.turned ? pack8(a) : x0[k];
+          *reinterpret_cast<uint4 *>(dst + n.e1) = n.turned ? pack8(b) : x1[k];
+        }
       }
     }
   }

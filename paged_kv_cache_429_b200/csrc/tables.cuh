@@ -14,12 +14,15 @@
 // stack first), and its token t (Q_s <= t < Q_s + n_s) stands at position
 // p = L_s + t - Q_s in slot table[s][p / 16] * 16 + p % 16.
 //
-// What bounds it: latency. A decode step reads and writes a few KB; the two
-// exclusive sums over the rows are the only dependence. Every CTA of one
-// cluster scans all the rows itself (two integers a row, from L2), so no
-// partial sums travel between CTAs; a cluster barrier stands between the
-// last read and the first write of the lengths and the count, which the
-// caller may update in place.
+// What bounds it: latency for a decode step (a few KB), the slots' and
+// positions' 12 bytes a token for large admissions. The two exclusive sums
+// over the rows are the only dependence: every CTA scans all the rows itself
+// (two integers a row, from L2) into shared memory, where the row of a token
+// or a block is then found by bisection, so no partial sums travel between
+// CTAs. The lengths and the count may be updated in place, so they are
+// written only when no CTA reads them any more: a small call is one CTA with
+// a barrier between, a large one a launch over the GPU for the tokens and a
+// one-CTA launch for the lengths and the count (TablePhase).
 #pragma once
 
 #include "decode.cuh"
@@ -27,24 +30,21 @@
 namespace pa {
 
 constexpr int kTabThreads = 1024;
-constexpr int kTabCluster = 8;            // CTAs of the (one) cluster
 constexpr int kTabMaxSeqs = 16384;        // rows whose sums one CTA's shared memory holds
-constexpr int kTokThreads = 256;
-constexpr int kTokPerThread = 4;
+constexpr int kTabBatch = 4;              // tokens or blocks of a thread in flight
+constexpr int kTabPerCta = kTabThreads * kTabBatch;
+constexpr int kTabSmallTokens = 2 * kTabPerCta;   // extend: one CTA up to here
+constexpr int kTabSmallBlocks = 8 * kTabPerCta;   // release: one CTA up to this bound of its pushes
 
 constexpr uint32_t kErrOutOfBlocks = 0x20u;
 constexpr uint32_t kErrLengthRange = 0x40u;
 constexpr uint32_t kErrFreeRange = 0x80u;
 
-__device__ __forceinline__ void cluster_sync_all() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
+enum class TablePhase {
+  kAll,     // one CTA
+  kWork,    // any number of CTAs: everything but the lengths and the count
+  kFinish,  // one CTA, after kWork: the lengths and the count
+};
 
 // Exclusive sums over the block's threads of two 64-bit counts (tokens of
 // up to 16384 rows can pass 32 bits); the totals go to every thread.
@@ -83,18 +83,20 @@ __device__ __forceinline__ Two block_exclusive_sum(Two v, Two &total) {
   return Two{before.a + x.a - v.a, before.b + x.b - v.b};
 }
 
-// Largest index i in [lo, hi) with start[i] <= v (start ascending,
-// start[lo] <= v).
-template <typename P>
-__device__ __forceinline__ int last_not_above(P start, int lo, int hi, int v) {
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (start[mid] <= v)
-      lo = mid;
-    else
-      hi = mid;
+// For each v[i]: the largest index k in [0, n) with start[k] <= v[i] (start
+// ascending, start[0] <= v[i]). A fixed number of halvings, the searches side
+// by side.
+template <int N>
+__device__ __forceinline__ void last_not_above(const int32_t *start, int n, const int (&v)[N], int (&k)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) k[i] = 0;
+  for (int step = n <= 1 ? 0 : 1 << (31 - __clz(n - 1)); step > 0; step >>= 1) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = k[i] + step;
+      if (c < n && start[c] <= v[i]) k[i] = c;
+    }
   }
-  return lo;
 }
 
 struct ExtendParams {
@@ -113,89 +115,122 @@ struct ExtendParams {
   int num_tokens;
   int num_blocks;               // pool size: ids are checked against it
   int free_capacity;
+  bool wide;                    // slot_mapping and positions are 16-byte aligned
 };
 
-// Lengths, count and new table entries: one cluster. Shared memory holds
-// the rows' exclusive block sums.
-__global__ void __launch_bounds__(kTabThreads) extend_rows_kernel(const ExtendParams p) {
-  extern __shared__ int32_t s_first[];  // [S + 1] blocks needed by earlier rows
+template <TablePhase PHASE>
+__global__ void __launch_bounds__(kTabThreads) extend_kernel(const ExtendParams p) {
+  extern __shared__ int32_t s_rows[];
   const int S = p.num_seqs;
+  int32_t *s_query = s_rows;           // [S + 1] tokens of earlier rows
+  int32_t *s_first = s_query + S + 1;  // [S] blocks needed by earlier rows
+  int32_t *s_len = s_first + S;        // [S]
   const int per = (S + kTabThreads - 1) / kTabThreads;
   const int s0 = min(S, static_cast<int>(threadIdx.x) * per), s1 = min(S, s0 + per);
   const int64_t row_cap = static_cast<int64_t>(p.max_blocks_per_seq) * kBS;
+  const int count = *p.free_count;
+  auto need = [](int64_t L, int64_t n) { return (L + n + kBS - 1) / kBS - (L + kBS - 1) / kBS; };
   Two mine{0, 0};
   bool bad = false;
   for (int s = s0; s < s1; ++s) {
     const int64_t L = p.context_lens[s], n = p.new_lens[s];
     bad |= L < 0 || n < 0 || L + n > row_cap;
     mine.a += n;
-    mine.b += (L + n + kBS - 1) / kBS - (L + kBS - 1) / kBS;
+    mine.b += need(L, n);
   }
-  const int count = *p.free_count;
   Two total;
   const Two first = block_exclusive_sum(mine, total);
   const bool length_bad = __syncthreads_or(bad) || total.a > p.num_tokens;
   const bool count_bad = count < 0 || count > p.free_capacity;
   const bool short_of = !length_bad && !count_bad && total.b > count;
   const bool ok = !length_bad && !count_bad && !short_of;
-  const uint32_t rank = cluster_rank();
-  if (!ok && rank == 0 && threadIdx.x == 0)
-    raise_error((length_bad ? kErrLengthRange : 0u) | (count_bad ? kErrFreeRange : 0u) |
-                (short_of ? kErrOutOfBlocks : 0u));
-  // the rows' sums; with nothing to do every sum is zero
-  int64_t q = first.a, b = first.b;
-  for (int s = s0; s < s1; ++s) {
-    s_first[s] = ok ? static_cast<int>(b) : 0;
-    if (rank == 0) p.query_start[s] = ok ? static_cast<int>(q) : 0;
-    const int64_t L = p.context_lens[s], n = p.new_lens[s];
-    q += n;
-    b += (L + n + kBS - 1) / kBS - (L + kBS - 1) / kBS;
+  if (PHASE != TablePhase::kWork) {
+    if (!ok && threadIdx.x == 0)
+      raise_error((length_bad ? kErrLengthRange : 0u) | (count_bad ? kErrFreeRange : 0u) |
+                  (short_of ? kErrOutOfBlocks : 0u));
   }
-  const int blocks = ok ? static_cast<int>(total.b) : 0;
-  if (threadIdx.x == 0) {
-    s_first[S] = blocks;
-    if (rank == 0) p.query_start[S] = ok ? static_cast<int>(total.a) : 0;
-  }
-  __syncthreads();
-  // new table entries, the cluster's threads side by side over the blocks
-  for (int k = rank * kTabThreads + threadIdx.x; k < blocks; k += kTabCluster * kTabThreads) {
-    const int s = last_not_above(s_first, 0, S, k);
-    const int old = (p.context_lens[s] + kBS - 1) / kBS;
-    p.block_tables[static_cast<int64_t>(s) * p.max_blocks_per_seq + old + k - s_first[s]] =
-        p.free_blocks[count - 1 - k];
-  }
-  cluster_sync_all();  // every CTA has read the lengths and the count
-  if (rank == 0) {
-    for (int s = threadIdx.x; s < S; s += kTabThreads)
-      p.context_lens_out[s] = p.context_lens[s] + (ok ? p.new_lens[s] : 0);
-    if (threadIdx.x == 0) *p.free_count_out = count - blocks;
-  }
-}
-
-// Slots and positions, four consecutive tokens a thread.
-__global__ void __launch_bounds__(kTokThreads) extend_tokens_kernel(const ExtendParams p) {
-  const int S = p.num_seqs;
-  const int total = p.query_start[S];
-  const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kTokThreads + threadIdx.x) * kTokPerThread;
-  int s = -1, end = -1;
-  for (int64_t t64 = t0; t64 < min(t0 + kTokPerThread, static_cast<int64_t>(p.num_tokens)); ++t64) {
-    const int t = static_cast<int>(t64);
-    int64_t slot = -1;
-    int pos = 0;
-    if (t < total) {
-      if (t >= end) {
-        s = last_not_above(p.query_start, 0, S, t);
-        end = p.query_start[s + 1];
-      }
-      pos = p.context_lens_out[s] - (end - t);
-      const int id = p.block_tables[static_cast<int64_t>(s) * p.max_blocks_per_seq + pos / kBS];
-      if (id >= 0 && id < p.num_blocks)
-        slot = static_cast<int64_t>(id) * kBS + pos % kBS;
-      else
-        raise_error(kErrBlockRange);
+  if (PHASE != TablePhase::kFinish) {
+    // the rows' sums; where nothing is to be done no token is live
+    const int tokens = ok ? static_cast<int>(total.a) : 0;
+    int64_t q = first.a, b = first.b;
+    for (int s = s0; s < s1; ++s) {
+      const int64_t L = p.context_lens[s], n = p.new_lens[s];
+      s_query[s] = ok ? static_cast<int>(q) : 0;
+      s_first[s] = static_cast<int>(b);
+      s_len[s] = static_cast<int>(L);
+      if (blockIdx.x == 0) p.query_start[s] = ok ? static_cast<int>(q) : 0;
+      q += n;
+      b += need(L, n);
     }
-    p.slot_mapping[t] = slot;
-    p.positions[t] = pos;
+    if (threadIdx.x == 0) {
+      s_query[S] = tokens;
+      if (blockIdx.x == 0) p.query_start[S] = tokens;
+    }
+    __syncthreads();
+    bool bad_id = false;
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * kTabPerCta;
+    for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kTabThreads + threadIdx.x) * kTabBatch;
+         t0 < p.num_tokens; t0 += stride) {
+      // four consecutive tokens: their rows (mostly one), then their block
+      // ids, then the stores
+      int t[kTabBatch], s[kTabBatch], pos[kTabBatch], id[kTabBatch];
+      int64_t slot[kTabBatch];
+#pragma unroll
+      for (int i = 0; i < kTabBatch; ++i) t[i] = static_cast<int>(min(t0 + i, static_cast<int64_t>(max(tokens - 1, 0))));
+      if (t0 < tokens) {
+        const int v[1] = {t[0]};
+        int k[1];
+        last_not_above(s_query, S, v, k);
+        if (t[kTabBatch - 1] < s_query[k[0] + 1]) {
+#pragma unroll
+          for (int i = 0; i < kTabBatch; ++i) s[i] = k[0];
+        } else {
+          last_not_above(s_query, S, t, s);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kTabBatch; ++i) {
+        pos[i] = 0;
+        id[i] = -1;
+        if (t0 + i < tokens) {
+          const int L = s_len[s[i]], old = (L + kBS - 1) / kBS;
+          pos[i] = L + t[i] - s_query[s[i]];
+          const int j = pos[i] / kBS;
+          int32_t *entry = p.block_tables + static_cast<int64_t>(s[i]) * p.max_blocks_per_seq + j;
+          if (j < old) {
+            id[i] = *entry;
+          } else {
+            id[i] = p.free_blocks[count - 1 - (s_first[s[i]] + j - old)];
+            if (pos[i] % kBS == 0) *entry = id[i];  // a new block begins with a new token
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kTabBatch; ++i) {
+        const bool in_pool = id[i] >= 0 && id[i] < p.num_blocks;
+        bad_id |= t0 + i < tokens && !in_pool;
+        slot[i] = in_pool ? static_cast<int64_t>(id[i]) * kBS + pos[i] % kBS : -1;
+      }
+      if (p.wide && t0 + kTabBatch <= p.num_tokens) {  // 16-byte stores
+        *reinterpret_cast<longlong2 *>(p.slot_mapping + t0) = make_longlong2(slot[0], slot[1]);
+        *reinterpret_cast<longlong2 *>(p.slot_mapping + t0 + 2) = make_longlong2(slot[2], slot[3]);
+        *reinterpret_cast<int4 *>(p.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kTabBatch; ++i)
+          if (t0 + i < p.num_tokens) {
+            p.slot_mapping[t0 + i] = slot[i];
+            p.positions[t0 + i] = pos[i];
+          }
+      }
+    }
+    if (bad_id) raise_error(kErrBlockRange);
+  }
+  if (PHASE != TablePhase::kWork) {
+    if (PHASE == TablePhase::kAll) __syncthreads();
+    for (int s = s0; s < s1; ++s)  // the rows this thread alone has read
+      p.context_lens_out[s] = p.context_lens[s] + (ok ? p.new_lens[s] : 0);
+    if (threadIdx.x == 0) *p.free_count_out = count - (ok ? static_cast<int>(total.b) : 0);
   }
 }
 
@@ -222,11 +257,13 @@ __device__ __forceinline__ int64_t released_blocks(const ReleaseParams &p, int s
 
 // Ended rows give back the blocks behind their first keep_blocks, row by
 // row, in table order.
-__global__ void __launch_bounds__(kTabThreads) release_rows_kernel(const ReleaseParams p) {
-  extern __shared__ int32_t s_first[];  // [S + 1] blocks pushed by earlier rows
+template <TablePhase PHASE>
+__global__ void __launch_bounds__(kTabThreads) release_kernel(const ReleaseParams p) {
+  extern __shared__ int32_t s_first[];  // [S] blocks pushed by earlier rows
   const int S = p.num_seqs;
   const int per = (S + kTabThreads - 1) / kTabThreads;
   const int s0 = min(S, static_cast<int>(threadIdx.x) * per), s1 = min(S, s0 + per);
+  const int count = *p.free_count;
   Two mine{0, 0};
   bool bad = false;
   for (int s = s0; s < s1; ++s) {
@@ -234,46 +271,47 @@ __global__ void __launch_bounds__(kTabThreads) release_rows_kernel(const Release
     bad |= p.release[s] != 0 && (L < 0 || L > static_cast<int64_t>(p.max_blocks_per_seq) * kBS);
     mine.b += released_blocks(p, s);
   }
-  const int count = *p.free_count;
   Two total;
   const Two first = block_exclusive_sum(mine, total);
   const bool length_bad = __syncthreads_or(bad);
   const bool count_bad =
       count < 0 || count > p.free_capacity || (!length_bad && count + total.b > p.free_capacity);
   const bool ok = !length_bad && !count_bad;
-  const uint32_t rank = cluster_rank();
-  if (!ok && rank == 0 && threadIdx.x == 0)
-    raise_error((length_bad ? kErrLengthRange : 0u) | (count_bad ? kErrFreeRange : 0u));
-  int64_t b = first.b;
-  for (int s = s0; s < s1; ++s) {
-    s_first[s] = ok ? static_cast<int>(b) : 0;
-    b += released_blocks(p, s);
-  }
   const int blocks = ok ? static_cast<int>(total.b) : 0;
-  if (threadIdx.x == 0) s_first[S] = blocks;
-  __syncthreads();
-  // one warp a row, the cluster's warps side by side
-  const int lane = threadIdx.x & 31;
-  bool bad_id = false;
-  for (int s = rank * (kTabThreads / 32) + (threadIdx.x >> 5); s < S;
-       s += kTabCluster * (kTabThreads / 32)) {
-    const int n = s_first[s + 1] - s_first[s];
-    const int32_t *row = p.block_tables + static_cast<int64_t>(s) * p.max_blocks_per_seq + p.keep_blocks;
-    for (int i = lane; i < n; i += 32) {
-      const int id = row[i];
-      bad_id |= id < 0 || id >= p.num_blocks;
-      p.free_blocks[count + s_first[s] + i] = id;
+  if (PHASE != TablePhase::kFinish) {
+    int64_t b = first.b;
+    for (int s = s0; s < s1; ++s) {
+      s_first[s] = static_cast<int>(b);
+      b += released_blocks(p, s);
     }
+    __syncthreads();
+    const int stride = gridDim.x * kTabThreads;
+    bool bad_id = false;
+    for (int64_t k0 = blockIdx.x * kTabThreads + threadIdx.x; k0 < blocks; k0 += kTabBatch * stride) {
+      int k[kTabBatch], s[kTabBatch], id[kTabBatch];
+#pragma unroll
+      for (int i = 0; i < kTabBatch; ++i) k[i] = static_cast<int>(min(k0 + i * stride, static_cast<int64_t>(blocks - 1)));
+      last_not_above(s_first, S, k, s);
+#pragma unroll
+      for (int i = 0; i < kTabBatch; ++i)
+        id[i] = p.block_tables[static_cast<int64_t>(s[i]) * p.max_blocks_per_seq + p.keep_blocks + k[i] - s_first[s[i]]];
+#pragma unroll
+      for (int i = 0; i < kTabBatch; ++i)
+        if (k0 + i * stride < blocks) {
+          bad_id |= id[i] < 0 || id[i] >= p.num_blocks;
+          p.free_blocks[count + k[i]] = id[i];
+        }
+    }
+    if (bad_id) raise_error(kErrBlockRange);
   }
-  if (bad_id) raise_error(kErrBlockRange);
-  cluster_sync_all();  // every CTA has read the lengths and the count
-  if (rank == 0) {
-    for (int s = threadIdx.x; s < S; s += kTabThreads) {
-      const int L = p.context_lens[s];
-      p.context_lens_out[s] =
-          (ok && p.release[s] != 0)
-              ? static_cast<int>(min(static_cast<int64_t>(L), static_cast<int64_t>(p.keep_blocks) * kBS))
-              : L;
+  if (PHASE != TablePhase::kWork) {
+    if (!ok && threadIdx.x == 0)
+      raise_error((length_bad ? kErrLengthRange : 0u) | (count_bad ? kErrFreeRange : 0u));
+    if (PHASE == TablePhase::kAll) __syncthreads();
+    for (int s = s0; s < s1; ++s) {  // the rows this thread alone has read
+      const int64_t L = p.context_lens[s];
+      p.context_lens_out[s] = static_cast<int>(
+          (ok && p.release[s] != 0) ? min(L, static_cast<int64_t>(p.keep_blocks) * kBS) : L);
     }
     if (threadIdx.x == 0) *p.free_count_out = count + blocks;
   }
