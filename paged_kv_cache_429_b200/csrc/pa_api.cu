@@ -219,10 +219,11 @@ size_t workspace_bytes_for(int num_seqs, int num_q_heads, int head_dim, int max_
 // (the workspace size must not depend on the device).
 struct SharedPlan {
   int row_tiles;      // CTAs along the rows: pairs of 128-row query tiles over all groups
-  int splits;         // parts of the longest prefix
+  int prefix_parts;   // CTAs along the longest prefix
+  int part_records;   // records each leaves
   int suffix_parts;   // parts of the longest suffix
   int part_len;
-  size_t o_bytes, m_bytes, bytes;  // 0 bytes: more parts than the grid has places
+  size_t pre_o, pre_ml, row_of, suf_o, suf_ml, bytes;  // places in the workspace, and its size
 };
 
 SharedPlan shared_plan(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int num_groups,
@@ -245,23 +246,51 @@ SharedPlan shared_plan(int num_seqs, int num_q_heads, int num_kv_heads, int head
       const int64_t cost = (units * used + kSms - 1) / kSms * (per + 2);
       if (cost < best) {
         best = cost;
-        s.splits = static_cast<int>(used);
+        s.prefix_parts = static_cast<int>(used);
+        s.part_records = static_cast<int>((per + pa::kSpRecordTiles - 1) / pa::kSpRecordTiles);
       }
     }
   }
-  // Suffix parts: about four waves of resident CTAs (3 per SM), at least 256 tokens each.
+  // Suffix parts: about four waves of resident CTAs (3 per SM), at least 256
+  // tokens each.
   const int64_t units = std::max<int64_t>(static_cast<int64_t>(num_seqs) * num_kv_heads, 1);
   const int64_t wanted = std::max<int64_t>(1, 4 * 3 * kSms / units);
   int64_t len = (max_suffix_len + wanted - 1) / wanted;
   len = std::max<int64_t>((len + 127) / 128 * 128, 256);
   s.part_len = static_cast<int>(std::min<int64_t>(len, INT32_MAX / 128 * 128));
-  const int64_t parts = std::max<int64_t>((static_cast<int64_t>(max_suffix_len) + s.part_len - 1) / s.part_len, 1);
-  s.suffix_parts = static_cast<int>(parts);
-  const int64_t rows = static_cast<int64_t>(num_seqs) * num_q_heads * (s.splits + parts);
-  s.o_bytes = (static_cast<size_t>(rows) * head_dim * 4 + 255) / 256 * 256;
-  s.m_bytes = (static_cast<size_t>(rows) * 4 + 255) / 256 * 256;
-  s.bytes = s.o_bytes + 2 * s.m_bytes;
+  s.suffix_parts = static_cast<int>(
+      std::max<int64_t>((static_cast<int64_t>(max_suffix_len) + s.part_len - 1) / s.part_len, 1));
+  const size_t pre_rows = static_cast<size_t>(s.prefix_parts) * s.part_records * num_kv_heads * 2 * s.row_tiles *
+                          pa::kSpRows;
+  const size_t suf_rows = static_cast<size_t>(s.suffix_parts) * num_seqs * num_q_heads;
+  const auto take = [&s](size_t n) {
+    const size_t at = s.bytes;
+    s.bytes += (n + 255) / 256 * 256;
+    return at;
+  };
+  s.pre_o = take(pre_rows * head_dim * 4);
+  s.pre_ml = take(pre_rows * 8);
+  s.row_of = take(static_cast<size_t>(num_seqs) * 4);
+  s.suf_o = take(suf_rows * head_dim * 4);
+  s.suf_ml = take(suf_rows * 8);
   return s;
+}
+
+// A launch that may start before the stream's kernel in front has finished
+// (the kernel itself waits for it before it reads what that one writes).
+template <typename... Params, typename... Args>
+pa_status launch_beside(void (*kern)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t st, Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 template <int D, bool FP8, int NT>
@@ -269,33 +298,36 @@ pa_status launch_shared_suffix(const CUtensorMap &tk, const CUtensorMap &tv, con
                                cudaStream_t st, int dev) {
   auto kern = pa::shared_suffix_kernel<D, FP8, NT>;
   static std::atomic<uint64_t> attr_done{0};
-  const size_t smem = pa::Plan<D, FP8, NT, false>::kSmemBytes;
+  constexpr size_t smem = pa::Plan<D, FP8, NT, false>::kSmemBytes;
   if (!ensure_smem_attr(kern, smem, attr_done, dev)) return PA_ERR_CUDA;
-  kern<<<dim3(p.suffix_parts, p.num_kv_heads, p.num_seqs), pa::kDecodeThreads, smem, st>>>(tk, tv, p);
+  const dim3 grid(p.suffix_parts, p.num_kv_heads, p.num_seqs);
+  if (p.row_tiles > 0) return launch_beside(kern, grid, pa::kDecodeThreads, smem, st, tk, tv, p);
+  kern<<<grid, pa::kDecodeThreads, smem, st>>>(tk, tv, p);
   return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 template <int D, bool FP8>
-pa_status launch_shared(const pa::SharedParams &p, int row_tiles, const void *k_cache, const void *v_cache,
-                        int rows, cudaStream_t st, int dev) {
+pa_status launch_shared(const pa::SharedParams &p, const void *k_cache, const void *v_cache, int rows,
+                        cudaStream_t st, int dev) {
   CUtensorMap tq, tk, tv;
   if (!make_q_tmap(&tq, p.q, p.num_seqs, p.num_q_heads, D, p.group, p.tokens_per_tile) ||
       !make_cache_tmap<D, FP8>(&tk, k_cache, rows) || !make_cache_tmap<D, FP8>(&tv, v_cache, rows))
     return PA_ERR_CUDA;
-  if (row_tiles > 0) {
+  if (p.row_tiles > 0) {
     auto kern = pa::shared_prefix_kernel<D, FP8>;
     static std::atomic<uint64_t> attr_done{0};
     using PL = pa::SpPlan<D, FP8>;
     if (!ensure_smem_attr(kern, PL::kSmemBytes, attr_done, dev)) return PA_ERR_CUDA;
-    kern<<<dim3(row_tiles, p.num_kv_heads, p.splits), PL::kThreads, PL::kSmemBytes, st>>>(tq, tk, tv, p);
+    kern<<<dim3(p.row_tiles, p.num_kv_heads, p.prefix_parts), PL::kThreads, PL::kSmemBytes, st>>>(tq, tk, tv, p);
     if (cudaGetLastError() != cudaSuccess) return PA_ERR_CUDA;
   }
   const pa_status rc = p.group <= 8 ? launch_shared_suffix<D, FP8, 1>(tk, tv, p, st, dev)
                                     : launch_shared_suffix<D, FP8, 2>(tk, tv, p, st, dev);
   if (rc != PA_OK) return rc;
-  const int64_t warps = static_cast<int64_t>(p.num_seqs) * p.num_q_heads;
-  pa::shared_join_kernel<D><<<static_cast<unsigned>((warps + 7) / 8), 256, 0, st>>>(p);
-  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  const int64_t head_rows = static_cast<int64_t>(p.num_seqs) * p.group;
+  const dim3 grid(static_cast<unsigned>((head_rows + pa::kJoinRows - 1) / pa::kJoinRows), p.num_kv_heads,
+                  D / pa::kJoinCols);
+  return launch_beside(pa::shared_join_kernel<D>, grid, 256, 0, st, p);
 }
 
 template <int D, bool FP8>
@@ -614,25 +646,28 @@ pa_status pa_decode_shared_prefix(float *out, const void *q, const void *k_cache
   p.out_scale = fp8 ? v_scale : 1.f;
   const SharedPlan plan = shared_plan(num_seqs, num_q_heads, num_kv_heads, head_dim, num_groups,
                                       max_prefix_blocks, max_suffix_len);
-  if (plan.bytes == 0) return PA_ERR_UNSUPPORTED;
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < plan.bytes) return PA_ERR_WORKSPACE;
   p.tokens_per_tile = pa::kSpRows / group;
-  p.splits = plan.splits;
+  p.prefix_parts = plan.prefix_parts;
+  p.part_records = plan.part_records;
   p.suffix_parts = plan.suffix_parts;
   p.part_len = plan.part_len;
+  p.row_tiles = plan.row_tiles;
   char *ws = static_cast<char *>(workspace);
-  p.ws_o = reinterpret_cast<float *>(ws);
-  p.ws_m = reinterpret_cast<float *>(ws + plan.o_bytes);
-  p.ws_l = reinterpret_cast<float *>(ws + plan.o_bytes + plan.m_bytes);
+  p.pre_o = reinterpret_cast<float *>(ws + plan.pre_o);
+  p.pre_ml = reinterpret_cast<float2 *>(ws + plan.pre_ml);
+  p.row_of = reinterpret_cast<int32_t *>(ws + plan.row_of);
+  p.suf_o = reinterpret_cast<float *>(ws + plan.suf_o);
+  p.suf_ml = reinterpret_cast<float2 *>(ws + plan.suf_ml);
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return PA_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int rows = static_cast<int>(rows64);
   if (head_dim == 128)
-    return fp8 ? launch_shared<128, true>(p, plan.row_tiles, k_cache, v_cache, rows, st, dev)
-               : launch_shared<128, false>(p, plan.row_tiles, k_cache, v_cache, rows, st, dev);
-  return fp8 ? launch_shared<64, true>(p, plan.row_tiles, k_cache, v_cache, rows, st, dev)
-             : launch_shared<64, false>(p, plan.row_tiles, k_cache, v_cache, rows, st, dev);
+    return fp8 ? launch_shared<128, true>(p, k_cache, v_cache, rows, st, dev)
+               : launch_shared<128, false>(p, k_cache, v_cache, rows, st, dev);
+  return fp8 ? launch_shared<64, true>(p, k_cache, v_cache, rows, st, dev)
+             : launch_shared<64, false>(p, k_cache, v_cache, rows, st, dev);
 }
 
 pa_status pa_prefill(float *out, const void *q, const void *k_cache, const void *v_cache,
