@@ -219,11 +219,10 @@ size_t workspace_bytes_for(int num_seqs, int num_q_heads, int head_dim, int max_
 // (the workspace size must not depend on the device).
 struct SharedPlan {
   int row_tiles;      // CTAs along the rows: pairs of 128-row query tiles over all groups
-  int prefix_parts;   // CTAs along the longest prefix
-  int part_records;   // records each leaves
+  int prefix_parts;   // parts of the longest prefix
   int suffix_parts;   // parts of the longest suffix
   int part_len;
-  size_t pre_o, pre_ml, row_of, suf_o, suf_ml, bytes;  // places in the workspace, and its size
+  size_t o_bytes, bytes;  // of the records' o, and of the whole workspace
 };
 
 SharedPlan shared_plan(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int num_groups,
@@ -235,19 +234,20 @@ SharedPlan shared_plan(int num_seqs, int num_q_heads, int num_kv_heads, int head
   s.row_tiles = groups > 0 && max_prefix_blocks > 0
                     ? static_cast<int>((num_seqs + groups * (per_cta - 1)) / per_cta)
                     : 0;
-  // Prefix parts: the number that makes waves x (key tiles of a part + 2)
-  // smallest; two tiles stand for a CTA's start and its output.
+  // Prefix parts, of at most kSpPartTiles key tiles: the number that makes
+  // waves x (key tiles of a part + 2) smallest; two tiles stand for a CTA's
+  // start and its output.
   if (s.row_tiles > 0) {
     const int64_t tiles = (max_prefix_blocks + pa::kSpBlocks - 1) / pa::kSpBlocks;
     const int64_t units = static_cast<int64_t>(s.row_tiles) * num_kv_heads;
+    const int64_t least = (tiles + pa::kSpPartTiles - 1) / pa::kSpPartTiles;
     int64_t best = INT64_MAX;
-    for (int64_t n = 1; n <= std::min<int64_t>(tiles, 128); ++n) {
+    for (int64_t n = least; n <= std::max<int64_t>(std::min<int64_t>(tiles, 128), least); ++n) {
       const int64_t per = (tiles + n - 1) / n, used = (tiles + per - 1) / per;
       const int64_t cost = (units * used + kSms - 1) / kSms * (per + 2);
       if (cost < best) {
         best = cost;
         s.prefix_parts = static_cast<int>(used);
-        s.part_records = static_cast<int>((per + pa::kSpRecordTiles - 1) / pa::kSpRecordTiles);
       }
     }
   }
@@ -260,19 +260,9 @@ SharedPlan shared_plan(int num_seqs, int num_q_heads, int num_kv_heads, int head
   s.part_len = static_cast<int>(std::min<int64_t>(len, INT32_MAX / 128 * 128));
   s.suffix_parts = static_cast<int>(
       std::max<int64_t>((static_cast<int64_t>(max_suffix_len) + s.part_len - 1) / s.part_len, 1));
-  const size_t pre_rows = static_cast<size_t>(s.prefix_parts) * s.part_records * num_kv_heads * 2 * s.row_tiles *
-                          pa::kSpRows;
-  const size_t suf_rows = static_cast<size_t>(s.suffix_parts) * num_seqs * num_q_heads;
-  const auto take = [&s](size_t n) {
-    const size_t at = s.bytes;
-    s.bytes += (n + 255) / 256 * 256;
-    return at;
-  };
-  s.pre_o = take(pre_rows * head_dim * 4);
-  s.pre_ml = take(pre_rows * 8);
-  s.row_of = take(static_cast<size_t>(num_seqs) * 4);
-  s.suf_o = take(suf_rows * head_dim * 4);
-  s.suf_ml = take(suf_rows * 8);
+  const size_t rows = (static_cast<size_t>(s.prefix_parts) + s.suffix_parts) * num_seqs * num_q_heads;
+  s.o_bytes = (rows * head_dim * 4 + 255) / 256 * 256;
+  s.bytes = s.o_bytes + (rows * 8 + 255) / 256 * 256;
   return s;
 }
 
@@ -324,10 +314,8 @@ pa_status launch_shared(const pa::SharedParams &p, const void *k_cache, const vo
   const pa_status rc = p.group <= 8 ? launch_shared_suffix<D, FP8, 1>(tk, tv, p, st, dev)
                                     : launch_shared_suffix<D, FP8, 2>(tk, tv, p, st, dev);
   if (rc != PA_OK) return rc;
-  const int64_t head_rows = static_cast<int64_t>(p.num_seqs) * p.group;
-  const dim3 grid(static_cast<unsigned>((head_rows + pa::kJoinRows - 1) / pa::kJoinRows), p.num_kv_heads,
-                  D / pa::kJoinCols);
-  return launch_beside(pa::shared_join_kernel<D>, grid, 256, 0, st, p);
+  const int64_t warps = static_cast<int64_t>(p.num_seqs) * p.num_q_heads;
+  return launch_beside(pa::shared_join_kernel<D>, dim3(static_cast<unsigned>((warps + 7) / 8)), 256, 0, st, p);
 }
 
 template <int D, bool FP8>
@@ -649,20 +637,17 @@ pa_status pa_decode_shared_prefix(float *out, const void *q, const void *k_cache
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < plan.bytes) return PA_ERR_WORKSPACE;
   p.tokens_per_tile = pa::kSpRows / group;
   p.prefix_parts = plan.prefix_parts;
-  p.part_records = plan.part_records;
   p.suffix_parts = plan.suffix_parts;
   p.part_len = plan.part_len;
   p.row_tiles = plan.row_tiles;
   char *ws = static_cast<char *>(workspace);
-  p.pre_o = reinterpret_cast<float *>(ws + plan.pre_o);
-  p.pre_ml = reinterpret_cast<float2 *>(ws + plan.pre_ml);
-  p.row_of = reinterpret_cast<int32_t *>(ws + plan.row_of);
-  p.suf_o = reinterpret_cast<float *>(ws + plan.suf_o);
-  p.suf_ml = reinterpret_cast<float2 *>(ws + plan.suf_ml);
+  p.rec_o = reinterpret_cast<float *>(ws);
+  p.rec_ml = reinterpret_cast<float2 *>(ws + plan.o_bytes);
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return PA_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int rows = static_cast<int>(rows64);
+  if (plan.prefix_parts > 65535) return PA_ERR_UNSUPPORTED;  // grid.z: prefixes above 134 million tokens
   if (head_dim == 128)
     return fp8 ? launch_shared<128, true>(p, k_cache, v_cache, rows, st, dev)
                : launch_shared<128, false>(p, k_cache, v_cache, rows, st, dev);

@@ -50,21 +50,16 @@ struct SharedParams {
   int group;                     // query heads per KV head
   int num_blocks;
   int tokens_per_tile;           // sequences of a 128-row query tile (128 / group, floor)
-  int prefix_parts;              // CTAs along the longest prefix
-  int part_records;              // records of a part (kSpRecordTiles)
+  int prefix_parts;              // parts of the longest prefix, a CTA (and a record) each
   int suffix_parts;              // suffix parts, part_len tokens each (the last one to the end)
   int part_len;
   float score_scale;             // sm_scale * log2(e) [* k_scale for fp8]
   float out_scale;               // v_scale for fp8, 1 for bf16
   int row_tiles;                 // CTAs along the prefix rows, two 128-row query tiles each
-  // Prefix records, o as 16-byte chunks in the order the tensor memory's
-  // rows lie in (thread r writes chunk c at [c][r], whole lines a warp):
-  float *pre_o;                  // [prefix_parts * part_records][Hkv][2 row_tiles][D / 4][128][4]
-  float2 *pre_ml;                // the same without chunks
-  int32_t *row_of;               // [S] a sequence's place among the tiles: tile * tokens_per_tile + place
-  // Suffix parts:
-  float *suf_o;                  // [suffix_parts][S * Hq][D]
-  float2 *suf_ml;                // [suffix_parts][S * Hq]
+  // Records, [prefix_parts + suffix_parts][S * Hq], the prefix's first: o
+  // [D] of each, and (m, l).
+  float *rec_o;
+  float2 *rec_ml;
 };
 
 // Flags groups that are not ascending inside the batch, and prefixes outside
@@ -96,25 +91,23 @@ __device__ __forceinline__ int shared_blocks_of(const SharedParams &p, int s) {
 constexpr int kSpRows = 128;                // rows of a query tile (MMA M)
 constexpr int kSpKeys = 128;                // keys of a prefix tile (score MMA N)
 constexpr int kSpBlocks = kSpKeys / kBS;
-// Most key tiles that add into one record. The tensor core's accumulator
-// truncates, so a sum over n tiles shrinks by about n * 2.6e-7 of itself
-// (measured: 8.3e-6 at 32 tiles); records are added up in fp32 by the join.
-constexpr int kSpRecordTiles = 16;
+// Most key tiles of a part. The tensor core's accumulator truncates, so a sum
+// over n tiles shrinks by about n * 2.6e-7 of itself (measured: 8.3e-6 at 32
+// tiles, and 1.35e-5 where all values have the same sign); the parts are
+// added up in fp32 by the join.
+constexpr int kSpPartTiles = 16;
 
 __host__ __device__ constexpr int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
-// How a prefix of `blocks` blocks is cut: parts (CTAs) of `tiles` key tiles,
-// each of `records` records of `record_tiles` tiles.
+// A prefix of `blocks` blocks cut into at most max_parts parts of `tiles` key tiles.
 struct PrefixCut {
-  int parts, tiles, records, record_tiles;
+  int parts, tiles;
 };
 __device__ __forceinline__ PrefixCut cut_prefix(int blocks, int max_parts) {
   PrefixCut c;
   const int all = ceil_div(blocks, kSpBlocks);
   c.tiles = ceil_div(all, max_parts);
   c.parts = ceil_div(all, c.tiles);
-  c.records = ceil_div(c.tiles, kSpRecordTiles);
-  c.record_tiles = ceil_div(c.tiles, c.records);
   return c;
 }
 
@@ -153,10 +146,8 @@ __device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontro
 // ------------------------------------------------------------ prefix parts
 
 constexpr int kSpSoftmaxWarps = 8;  // two warpgroups
-// Largest sum of 64 weights against an older reference: bf16 halves have
-// fp32's range, f16 ones reach 2^16.
-constexpr float kSpSumMaxBf16 = 1.0e18f;
-constexpr float kSpSumMaxF16 = 32768.f;
+constexpr float kSpSumMaxBf16 = 1.0e18f;   // a tile's weights against an older maximum
+constexpr float kSpSumMaxF16 = 32768.f;    // f16 halves: every weight <= 2^15
 constexpr float kSpF16Log2 = 8.f;          // f16 weights are 2^(z - m + 8): small ones keep bits
 
 template <int D, bool FP8>
@@ -170,7 +161,7 @@ struct SpPlan {
   static_assert(FP8 ? 2 * kSoftmaxRegs + kIssueRegs + kConvertRegs <= 4 * 128
                     : 2 * kSoftmaxRegs + kIssueRegs <= 3 * 168,
                 "register split");
-  static constexpr int kIssueWarp0 = kThreads / 32 - 4;  // K (and Q) loads, V loads, two MMA warps
+  static constexpr int kIssueWarp0 = kThreads / 32 - 4;  // K (and Q) loads, V loads, MMA, idle
   static constexpr int kHalves = D / 64;
   static constexpr int kHalfBytes = kSpRows * 128;       // [128 rows][64 elements of 16 bits]
   static constexpr int kTileBytes = kHalves * kHalfBytes;  // a Q, K or V operand tile
@@ -184,8 +175,8 @@ struct SpPlan {
   static constexpr int kVbOff = kKbOff + kNB * kByteTile;
   static constexpr int kBarOff = kVbOff + kNB * kByteTile;
   // q_full[2] q_conv[2] k_full[NK] k_empty[NK] v_full[NV] v_empty[NV]
-  // kb_full[2] kb_empty[2] vb_full[2] vb_empty[2] s_full[2] p_full[2][2] o_half[2] o_done[2] drain[2]
-  static constexpr int kNumBars = 4 + 2 * kNK + 2 * kNV + 8 + 10 + 2;
+  // kb_full[2] kb_empty[2] vb_full[2] vb_empty[2] s_full[2] p_full[2] o_done[2] drain
+  static constexpr int kNumBars = 4 + 2 * kNK + 2 * kNV + 8 + 6 + 1;
   static constexpr int kSmemBytes = 1024 + kBarOff + 8 * kNumBars + 16;
   static constexpr int kTmemCols = 512;
   static constexpr int kOCol = 2 * kSpKeys;
@@ -202,9 +193,11 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
   return v;
 }
 
-// Arrive at named barrier `id` without waiting (its other threads sync).
-__device__ __forceinline__ void named_bar_arrive(uint32_t id, uint32_t count) {
-  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
+// 32 bytes, a whole sector, of one thread (32-byte aligned).
+__device__ __forceinline__ void st_global_v8(float *p, const uint32_t *v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 
 // Byte of 16-byte chunk c (0..7) of row r in one 64-element half of an
@@ -220,7 +213,6 @@ __global__ void __launch_bounds__(SpPlan<D, FP8>::kThreads, 1)
                          const __grid_constant__ CUtensorMap tmap_v, const SharedParams p) {
   using PL = SpPlan<D, FP8>;
   constexpr int H = PL::kHalves, NK = PL::kNK, NV = PL::kNV, NB = PL::kNB;
-  // K and V loads; the MMAs of slot 0 and of slot 1
   constexpr int kKWarp = PL::kIssueWarp0, kVWarp = kKWarp + 1, kMmaWarp = kKWarp + 2;
 
   extern __shared__ uint8_t smem_raw[];
@@ -240,9 +232,8 @@ __global__ void __launch_bounds__(SpPlan<D, FP8>::kThreads, 1)
   const uint32_t bar_vb_full = bar_kb_empty + 16;
   const uint32_t bar_vb_empty = bar_vb_full + 16;
   const uint32_t bar_s_full = bar_vb_empty + 16;      // [tile]
-  const uint32_t bar_p_full = bar_s_full + 16;        // [tile][half of the keys]
-  const uint32_t bar_o_half = bar_p_full + 32;        // [tile] the first half's product
-  const uint32_t bar_o_done = bar_o_half + 16;        // [tile]
+  const uint32_t bar_p_full = bar_s_full + 16;        // [tile]
+  const uint32_t bar_o_done = bar_p_full + 16;        // [tile]
   const uint32_t bar_drain = bar_o_done + 16;
   uint32_t *s_tmem = reinterpret_cast<uint32_t *>(base_ptr + PL::kBarOff + 8 * PL::kNumBars);
   volatile int *s_abort = reinterpret_cast<volatile int *>(s_tmem + 1);
@@ -293,8 +284,6 @@ __global__ void __launch_bounds__(SpPlan<D, FP8>::kThreads, 1)
   const int nblk = min(blocks - blk0, cut.tiles * kSpBlocks);
   if (nblk <= 0) return;  // no such part of this prefix
   const int nt = ceil_div(nblk, kSpBlocks);
-  if (h == 0 && part == 0)
-    for (int i = threadIdx.x; i < nseq; i += PL::kThreads) p.row_of[seq0 + i] = blockIdx.x * 2 * tpt + i;
   // One query tile only: both softmax warpgroups take it, with alternate key
   // tiles, and their results are joined at the end.
   const bool alternate = nseq <= tpt;
@@ -305,10 +294,7 @@ __global__ void __launch_bounds__(SpPlan<D, FP8>::kThreads, 1)
       mbar_init(bar_q + 8u * g, 1);
       mbar_init(bar_qc + 8u * g, 128);
       mbar_init(bar_s_full + 8u * g, 1);
-      mbar_init(bar_p_full + 16u * g, 4);  // a warp each
-      mbar_init(bar_p_full + 16u * g + 8u, 4);
-      mbar_init(bar_drain + 8u * g, 1);
-      mbar_init(bar_o_half + 8u * g, 1);
+      mbar_init(bar_p_full + 8u * g, 128);
       mbar_init(bar_o_done + 8u * g, 1);
       mbar_init(bar_kb_full + 8u * g, 1);
       mbar_init(bar_kb_empty + 8u * g, 128);
@@ -317,12 +303,13 @@ __global__ void __launch_bounds__(SpPlan<D, FP8>::kThreads, 1)
     }
     for (int i = 0; i < NK; ++i) {
       mbar_init(bar_k_full + 8u * i, FP8 ? 128 : 1);
-      mbar_init(bar_k_empty + 8u * i, alternate ? 1 : 2);  // both slots read a tile
+      mbar_init(bar_k_empty + 8u * i, 1);
     }
     for (int i = 0; i < NV; ++i) {
       mbar_init(bar_v_full + 8u * i, FP8 ? 128 : 1);
-      mbar_init(bar_v_empty + 8u * i, alternate ? 1 : 2);
+      mbar_init(bar_v_empty + 8u * i, 1);
     }
+    mbar_init(bar_drain, 1);
     *s_abort = 0;
     fence_barrier_init();
   }
@@ -408,72 +395,105 @@ __global__ void __launch_bounds__(SpPlan<D, FP8>::kThreads, 1)
         for (int j = max(0, issued - nst); j < issued; ++j)
           mbar_wait_bounded(bar_full + 8u * (j % nst), (j / nst) & 1, kWaitLimitNs);
       }
-    } else {
+    } else if (warp == kMmaWarp) {
       // ------------------------------------------------------------- MMA
-      // A thread for each slot g, so that neither waits for the other's
-      // softmax: S_g(0), then PV_g(n), S_g(n+1). S_g(n+1) overwrites the
-      // columns PV_g(n) reads and is issued behind it (one thread's MMAs run
-      // in issue order).
-      const int g = warp - kMmaWarp;
-      const int ntg = g == 0 ? my_tiles0 : my_tiles1;
-      if (lane == 0 && ntg > 0) {
+      if (lane == 0) {
         constexpr uint32_t id_s = FP8 ? tc_idesc_f16(kSpRows, kSpKeys, false) : tc_idesc_bf16(kSpRows, kSpKeys, false);
         constexpr uint32_t id_pv = FP8 ? tc_idesc_f16(kSpRows, D, true) : tc_idesc_bf16(kSpRows, D, true);
-        const int qt = alternate ? 0 : g;
-        const uint32_t qst = sq + qt * PL::kTileBytes;
-        const uint32_t st = tmem + g * kSpKeys, o = tmem + PL::kOCol + g * D;
-        auto tile_of = [&](int n) { return alternate ? 2 * n + g : n; };
-        bool ok = tc_wait((FP8 ? bar_qc : bar_q) + 8u * qt, 0, s_abort);
-        // scores of the n-th key tile into the slot's columns
-        auto issue_s = [&](int n) {
-          const int j = tile_of(n);
+        bool ok = true;
+        auto wait_k = [&](int j) {
           ok = ok && tc_wait(bar_k_full + 8u * (j % NK), (j / NK) & 1, s_abort);
-          if (!ok) return;
           tc_fence_after_sync();
+        };
+        auto wait_q = [&](int g) {
+          ok = ok && tc_wait((FP8 ? bar_qc : bar_q) + 8u * g, 0, s_abort);
+          tc_fence_after_sync();
+        };
+        // P of tile slot g's n-th key tile, and V of key tile j
+        auto wait_pv = [&](int g, int n, int j) {
+          ok = ok && tc_wait(bar_p_full + 8u * g, n & 1, s_abort) &&
+               tc_wait(bar_v_full + 8u * (j % NV), (j / NV) & 1, s_abort);
+          tc_fence_after_sync();
+        };
+        // scores of query tile qt against key tile j, into slot g's columns
+        auto issue_s = [&](int g, int qt, int j) {
           const uint32_t kst = sk + (j % NK) * PL::kTileBytes;
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
             const uint32_t off = (ks >> 2) * PL::kHalfBytes + (ks & 3) * 32;
-            tc_mma_ss(st, tc_desc_sw128(qst + off, 16, 1024), tc_desc_sw128(kst + off, 16, 1024), id_s, ks > 0);
+            tc_mma_ss(tmem + g * kSpKeys, tc_desc_sw128(sq + qt * PL::kTileBytes + off, 16, 1024),
+                      tc_desc_sw128(kst + off, 16, 1024), id_s, ks > 0);
           }
           tc_commit(bar_s_full + 8u * g);
-          tc_commit(bar_k_empty + 8u * (j % NK));
         };
-        issue_s(0);
-        for (int n = 0; n < ntg && ok; ++n) {
-          const int j = tile_of(n);
+        // O_g += (hi + lo) V: the halves of P in slot g's columns, hi first
+        auto issue_pv = [&](int g, int j, bool accumulate) {
           const uint32_t vst = sv + (j % NV) * PL::kTileBytes;
-          // O += (hi + lo) V, the first 64 keys as soon as their weights are
-          // there; a record's first tile overwrites
-          const bool fresh = n % cut.record_tiles == 0;
-          // one stage and two readers: the other slot's phase first (a parity
-          // wait cannot tell a phase from the one two before)
-          if (NV == 1 && alternate && j > 0) ok = tc_wait(bar_v_full, (j - 1) & 1, s_abort);
-          ok = ok && tc_wait(bar_v_full + 8u * (j % NV), (j / NV) & 1, s_abort);
+          const uint32_t pt = tmem + g * kSpKeys, o = tmem + PL::kOCol + g * D;
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            ok = ok && tc_wait(bar_p_full + 16u * g + 8u * half, n & 1, s_abort);
-            if (!ok) break;
-            tc_fence_after_sync();
-#pragma unroll
-            for (int kk = 0; kk < kSpBlocks; ++kk) {
-              const int k16 = kk % (kSpBlocks / 2), lo = kk / (kSpBlocks / 2);
-              tc_mma_ts(o, st + half * 64 + lo * 32 + k16 * 8,
-                        tc_desc_sw128(vst + (half * (kSpBlocks / 2) + k16) * 2048, PL::kHalfBytes, 1024), id_pv,
-                        !fresh || half > 0 || kk > 0);
-            }
-            if (half == 0) tc_commit(bar_o_half + 8u * g);
+          for (int kk = 0; kk < 2 * kSpBlocks; ++kk)
+            tc_mma_ts(o, pt + kk * 8, tc_desc_sw128(vst + (kk % kSpBlocks) * 2048, PL::kHalfBytes, 1024), id_pv,
+                      accumulate || kk > 0);
+        };
+        if (!alternate) {
+          wait_q(0);
+          wait_q(1);
+          wait_k(0);
+          if (ok) {
+            issue_s(0, 0, 0);
+            issue_s(1, 1, 0);
+            tc_commit(bar_k_empty);
           }
-          if (!ok) break;
-          tc_commit(bar_v_empty + 8u * (j % NV));
-          if (n + 1 < ntg)
-            issue_s(n + 1);
-          else
-            tc_commit(bar_o_done + 8u * g);
+          // PV_0(j), S_0(j+1), PV_1(j), S_1(j+1): S_g(j+1) overwrites the
+          // columns PV_g(j) reads and is issued behind it
+          for (int j = 0; j < nt && ok; ++j) {
+            const bool next = j + 1 < nt;
+            wait_pv(0, j, j);
+            if (!ok) break;
+            issue_pv(0, j, j > 0);
+            if (!next) tc_commit(bar_o_done);
+            if (next) {
+              wait_k(j + 1);
+              if (!ok) break;
+              issue_s(0, 0, j + 1);
+            }
+            wait_pv(1, j, j);
+            if (!ok) break;
+            issue_pv(1, j, j > 0);
+            if (!next) tc_commit(bar_o_done + 8u);
+            tc_commit(bar_v_empty + 8u * (j % NV));
+            if (next) {
+              issue_s(1, 1, j + 1);
+              tc_commit(bar_k_empty + 8u * ((j + 1) % NK));
+            }
+          }
+        } else {
+          wait_q(0);
+          for (int j = 0; j < min(nt, 2) && ok; ++j) {
+            wait_k(j);
+            if (!ok) break;
+            issue_s(j, 0, j);
+            tc_commit(bar_k_empty + 8u * (j % NK));
+          }
+          for (int j = 0; j < nt && ok; ++j) {
+            const int g = j & 1;
+            wait_pv(g, j >> 1, j);
+            if (!ok) break;
+            issue_pv(g, j, j > 1);
+            tc_commit(bar_v_empty + 8u * (j % NV));
+            if (j + 2 >= nt) {
+              tc_commit(bar_o_done + 8u * g);
+            } else {
+              wait_k(j + 2);
+              if (!ok) break;
+              issue_s(g, 0, j + 2);
+              tc_commit(bar_k_empty + 8u * (j % NK));
+            }
+          }
         }
         // every MMA issued here has completed before tensor memory is freed
-        tc_commit(bar_drain + 8u * g);
-        mbar_wait_bounded(bar_drain + 8u * g, 0, kWaitLimitNs);
+        tc_commit(bar_drain);
+        mbar_wait_bounded(bar_drain, 0, kWaitLimitNs);
       }
       __syncwarp();
     }
@@ -528,7 +548,7 @@ __global__ void __launch_bounds__(SpPlan<D, FP8>::kThreads, 1)
     const int g = warp >> 2;                       // slot of this warpgroup
     const int quarter = warp & 3;
     const int r = quarter * 32 + lane;             // row = tensor-memory lane
-    const int tl = r / p.group;
+    const int tl = r / p.group, nh = r - tl * p.group;
     const int sl = (alternate ? 0 : g * tpt) + tl; // sequence of the CTA's stretch
     const bool valid = tl < tpt && sl < nseq;
     const uint32_t trow = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
@@ -579,146 +599,120 @@ __global__ void __launch_bounds__(SpPlan<D, FP8>::kThreads, 1)
         mbar_arrive(bar_qc + 8u * g);
       }
     }
-    // record `rec` of this part, this warpgroup's rows (tile 0's, where both take it)
-    auto record_at = [&](int rec) {
-      return ((static_cast<int64_t>(part) * p.part_records + rec) * p.num_kv_heads + h) * (2 * p.row_tiles) +
-             2 * blockIdx.x + (alternate ? 0 : g);
-    };
-    constexpr float kSumMax = FP8 ? kSpSumMaxF16 : kSpSumMaxBf16;
     float m_used = -INFINITY, l = 0.f;
-    // slot g's sums so far as record `rec`
-    auto write_record = [&](int rec) {
-      const int64_t at = record_at(rec);
-      float4 *dst = reinterpret_cast<float4 *>(p.pre_o) + at * (D / 4) * kSpRows + r;
-#pragma unroll
-      for (int cc = 0; cc < D / 32; ++cc) {
-        uint32_t o[32];
-        tc_ld_32x32b_x32(trow + ocol + cc * 32, o);
-        tc_wait_ld();
-#pragma unroll
-        for (int e = 0; e < 32; e += 4)
-          dst[(cc * 8 + e / 4) * kSpRows] = make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
-                                                        __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
-      }
-      p.pre_ml[at * kSpRows + r] = make_float2(m_used, l);
-    };
-    // Records in the order they are written: with alternate key tiles the
-    // first warpgroup's, the second's, and last the joined rest of both.
-    int rec = (alternate && g == 1) ? (my_tiles0 - 1) / cut.record_tiles : 0;
-    // The two warpgroups take turns at the exponentials (named barriers 4 and
-    // 5, a turn of slot 0 and of slot 1): left alone they fall into step,
-    // because they share the key tiles, and the tensor core idles while both
-    // compute. Every turn is passed on, whatever was aborted.
-    const int other_tiles = g == 0 ? my_tiles1 : my_tiles0;
-    if (g == 1 && my_tiles0 > 0) named_bar_arrive(4, 256);
-    for (int n = 0; n < ntg; ++n) {
+    for (int n = 0; n < ntg && ok; ++n) {
       const int j = alternate ? 2 * n + g : n;     // key tile
-      if (ok) ok = __all_sync(0xffffffffu, tc_wait(bar_s_full + 8u * g, n & 1, s_abort));
+      ok = __all_sync(0xffffffffu, tc_wait(bar_s_full + 8u * g, n & 1, s_abort));
+      if (!ok) break;
       tc_fence_after_sync();
-      const bool fresh = n % cut.record_tiles == 0;
-      if (ok && fresh && n > 0) {  // the earlier tiles' products completed before these scores
-        write_record(rec++);
-        l = 0.f;
+      uint32_t sr[4][32];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) tc_ld_32x32b_x32(trow + scol + 32 * x, sr[x]);
+      tc_wait_ld();
+      float z[kSpKeys];
+#pragma unroll
+      for (int c = 0; c < kSpKeys; ++c) z[c] = __uint_as_float(sr[c >> 5][c & 31]);
+      // keys past the part's last block (the last tile's, loaded as zeros)
+      const int keys = nblk * kBS - j * kSpKeys;
+      float mul = scale;
+      if (keys < kSpKeys) {  // scaled here: a masked key is -inf whatever the scale's sign
+#pragma unroll
+        for (int c = 0; c < kSpKeys; ++c) z[c] = c < keys ? z[c] * scale : -INFINITY;
+        mul = 1.f;
       }
-      uint32_t sr[2][64];
-      if (ok) {
-        tc_ld_cols<64>(trow + scol, sr[0]);
-        tc_ld_cols<64>(trow + scol + 64, sr[1]);
-        tc_wait_ld();
-      }
-      named_bar_sync(4 + g, 256);
-      const int keys = nblk * kBS - j * kSpKeys;   // keys past the part's last block: loaded as zeros
-      // A softmax is the same for any reference m, and the halves keep their
-      // relative precision as long as the weights stay in the type's range. A
-      // row's first 64 keys take their maximum first; any later 64 are formed
-      // against the reference in use, without a maximum, and only where their
-      // sum leaves the range formed again against a raised one. 64 keys go to
-      // the MMA warp while the next are formed; P overwrites their scores:
-      // hi in the first 32 columns, lo in the last 32.
+      uint64_t lsum[2];
+      // P = 2^(z mul - m) in two 16-bit halves over the score columns: hi
+      // in the first 64, lo in the last 64; l sums P in fp32
+      auto form_p = [&](float neg_m) {
+        const uint64_t sc2 = f2(mul, mul), nm2 = f2(neg_m, neg_m);
+        lsum[0] = lsum[1] = f2(0.f, 0.f);
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        if (!ok) break;
-        const uint32_t col = trow + scol + 64 * half;
-        float mul = scale;
-        if (keys < 64 * half + 64) {  // scaled here: a masked key is -inf whatever the scale's sign
+        for (int qq = 0; qq < 4; ++qq) {
+          uint32_t hi[16], lo[16];
 #pragma unroll
-          for (int c = 0; c < 64; ++c)
-            sr[half][c] = __float_as_uint(64 * half + c < keys ? __uint_as_float(sr[half][c]) * scale : -INFINITY);
-          mul = 1.f;
-        }
-        float sum = 0.f;
-        auto form = [&]() {
-          const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
-          const uint64_t sc2 = f2(mul, mul), nm2 = f2(neg_m, neg_m);
-          uint64_t lsum[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
-#pragma unroll
-          for (int qq = 0; qq < 2; ++qq) {
-            uint32_t hi[16], lo[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const int c = 32 * qq + 2 * e;
-              float x0, x1, u0, u1;
-              f2_split(f2_fma(f2(__uint_as_float(sr[half][c]), __uint_as_float(sr[half][c + 1])), sc2, nm2), x0, x1);
-              const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-              hi[e] = pack2<FP8>(p0, p1);
-              unpack2<FP8>(hi[e], u0, u1);
-              lo[e] = pack2<FP8>(p0 - u0, p1 - u1);
-              lsum[e & 1] = f2_add(lsum[e & 1], f2(p0, p1));
-            }
-            tc_st_32x32b_x16(col + 16 * qq, hi);
-            tc_st_32x32b_x16(col + 32 + 16 * qq, lo);
+          for (int e = 0; e < 16; ++e) {
+            const int c = 32 * qq + 2 * e;
+            float x0, x1, u0, u1;
+            f2_split(f2_fma(f2(z[c], z[c + 1]), sc2, nm2), x0, x1);
+            const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+            hi[e] = pack2<FP8>(p0, p1);
+            unpack2<FP8>(hi[e], u0, u1);
+            lo[e] = pack2<FP8>(p0 - u0, p1 - u1);
+            lsum[e & 1] = f2_add(lsum[e & 1], f2(p0, p1));
           }
-          float a0, a1, b0, b1;
-          f2_split(lsum[0], a0, a1);
-          f2_split(lsum[1], b0, b1);
-          sum = (a0 + b0) + (a1 + b1);
-        };
-        bool redo = !__all_sync(0xffffffffu, !valid || m_used != -INFINITY);
-        if (!redo) {
-          form();
-          redo = __any_sync(0xffffffffu, valid && !(sum <= kSumMax));
+          tc_st_32x32b_x16(trow + scol + 16 * qq, hi);
+          tc_st_32x32b_x16(trow + scol + 64 + 16 * qq, lo);
         }
-        if (redo) {
-          tc_wait_st();  // the same columns are written again
-          float mx = __uint_as_float(sr[half][0]);  // the largest argument is that of an end of the scores
-#pragma unroll
-          for (int c = 1; c < 64; ++c)
-            mx = mul >= 0.f ? fmaxf(mx, __uint_as_float(sr[half][c])) : fminf(mx, __uint_as_float(sr[half][c]));
-          const float m_new = fmaxf(m_used, mx * mul - (FP8 ? kSpF16Log2 : 0.f));
-          const float alpha = m_new == m_used ? 1.f : ex2_approx(m_used - m_new);
-          m_used = m_new;
-          l *= alpha;
-          // Earlier tiles' products completed before these scores; that of
-          // this tile's first half has a barrier of its own.
-          if (half == 1) ok = __all_sync(0xffffffffu, tc_wait(bar_o_half + 8u * g, n & 1, s_abort));
-          if ((half == 1 || !fresh) && __any_sync(0xffffffffu, alpha != 1.f)) {
-            tc_fence_after_sync();
-#pragma unroll 1
-            for (int cc = 0; cc < D / 32; ++cc) {
-              uint32_t o[32];
-              tc_ld_32x32b_x32(trow + ocol + cc * 32, o);
-              tc_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-              tc_st_32x32b_x32(trow + ocol + cc * 32, o);
-            }
-          }
-          form();
-        }
-        l += sum;
-        tc_wait_st();
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar_p_full + 16u * g + 8u * half);
+      };
+      auto tile_sum = [&]() {
+        float a0, a1, b0, b1;
+        f2_split(lsum[0], a0, a1);
+        f2_split(lsum[1], b0, b1);
+        return (a0 + b0) + (a1 + b1);
+      };
+      // A row's first tile takes its maximum first. Any later one is formed
+      // against the reference in use: a softmax is the same for any
+      // reference, and the halves keep their relative precision as long as
+      // the weights stay in the type's range, which the tile's sum tells.
+      constexpr float kSumMax = FP8 ? kSpSumMaxF16 : kSpSumMaxBf16;
+      bool redo = true;
+      if (__all_sync(0xffffffffu, !valid || m_used != -INFINITY)) {
+        form_p(m_used == -INFINITY ? 0.f : -m_used);
+        redo = __any_sync(0xffffffffu, valid && !(tile_sum() <= kSumMax));
+        if (redo) tc_wait_st();  // the second pass rewrites the same columns
       }
-      // slot 1 follows slot 0's n-th turn, slot 0's (n+1)-th slot 1's n-th
-      if (g == 0 ? n < other_tiles : n + 1 < other_tiles) named_bar_arrive(5 - g, 256);
+      if (redo) {
+        float mx = z[0];
+#pragma unroll
+        for (int c = 1; c + 1 < kSpKeys; c += 2) mx = fmax3(mx, z[c], z[c + 1]);
+        mx = fmaxf(mx, z[kSpKeys - 1]);
+        if (mul < 0.f) {  // then the largest argument is the smallest score's
+          mx = z[0];
+#pragma unroll
+          for (int c = 1; c < kSpKeys; ++c) mx = fminf(mx, z[c]);
+        }
+        const float m_new = fmaxf(m_used, mx * mul - (FP8 ? kSpF16Log2 : 0.f));
+        const float alpha = m_new == m_used ? 1.f : ex2_approx(m_used - m_new);
+        m_used = m_new;
+        l *= alpha;
+        form_p(m_used == -INFINITY ? 0.f : -m_used);
+        if (n > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+          // O_g holds the earlier products: they completed before these scores
+#pragma unroll
+          for (int cc = 0; cc < D / 32; ++cc) {
+            uint32_t o[32];
+            tc_ld_32x32b_x32(trow + ocol + cc * 32, o);
+            tc_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tc_st_32x32b_x32(trow + ocol + cc * 32, o);
+          }
+        }
+      }
+      l += tile_sum();
+      tc_wait_st();
+      tc_fence_before_sync();
+      mbar_arrive(bar_p_full + 8u * g);
     }
     // ------------------------------------------------------------ epilogue
     if (ok && ntg > 0) ok = __all_sync(0xffffffffu, tc_wait(bar_o_done + 8u * g, 0, s_abort));
     tc_fence_after_sync();
+    const int64_t at = (static_cast<int64_t>(part) * p.num_seqs + seq0 + sl) * p.num_q_heads + h * p.group + nh;
+    float *dst = p.rec_o + at * D;
     if (!alternate || nt == 1) {
-      if (ok && ntg > 0) write_record(rec);
+      if (ok && ntg > 0) {
+#pragma unroll 1
+        for (int cc = 0; cc < D / 32; ++cc) {
+          uint32_t o[32];
+          tc_ld_32x32b_x32(trow + ocol + cc * 32, o);
+          tc_wait_ld();
+          if (valid) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) st_global_v8(dst + cc * 32 + e, o + e);
+          }
+        }
+        if (valid) p.rec_ml[at] = make_float2(m_used, l);
+      }
     } else {
       // Both warpgroups hold a share of the same rows. Every MMA and copy has
       // completed once both have seen their last product, so the second
@@ -726,9 +720,8 @@ __global__ void __launch_bounds__(SpPlan<D, FP8>::kThreads, 1)
       ok = named_bar_and(3, 256, ok);
       float4 *so = reinterpret_cast<float4 *>(base_ptr + PL::kKOff);    // [D / 4][128]
       float2 *sml = reinterpret_cast<float2 *>(base_ptr + PL::kTileBytes);  // query tile 1's place
-      rec = (my_tiles0 - 1) / cut.record_tiles + (my_tiles1 - 1) / cut.record_tiles;
       if (ok && g == 1) {
-#pragma unroll
+#pragma unroll 1
         for (int cc = 0; cc < D / 32; ++cc) {
           uint32_t o[32];
           tc_ld_32x32b_x32(trow + ocol + cc * 32, o);
@@ -743,31 +736,31 @@ __global__ void __launch_bounds__(SpPlan<D, FP8>::kThreads, 1)
       }
       named_bar_sync(3, 256);
       if (ok && g == 0) {
-        const int64_t at = record_at(rec);
-        float4 *dst = reinterpret_cast<float4 *>(p.pre_o) + at * (D / 4) * kSpRows + r;
         const float2 other = sml[r];
         const float M = fmaxf(m_used, other.x);
         const float wa = M == -INFINITY ? 0.f : ex2_approx(m_used - M);
         const float wb = M == -INFINITY ? 0.f : ex2_approx(other.x - M);
-#pragma unroll
+#pragma unroll 1
         for (int cc = 0; cc < D / 32; ++cc) {
           uint32_t o[32];
           tc_ld_32x32b_x32(trow + ocol + cc * 32, o);
           tc_wait_ld();
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
-            const float4 x = so[(cc * 8 + e / 4) * kSpRows + r];
-            dst[(cc * 8 + e / 4) * kSpRows] =
-                make_float4(wa * __uint_as_float(o[e]) + wb * x.x, wa * __uint_as_float(o[e + 1]) + wb * x.y,
-                            wa * __uint_as_float(o[e + 2]) + wb * x.z, wa * __uint_as_float(o[e + 3]) + wb * x.w);
+            const float4 y = so[(cc * 8 + e / 4) * kSpRows + r];
+            o[e] = __float_as_uint(wa * __uint_as_float(o[e]) + wb * y.x);
+            o[e + 1] = __float_as_uint(wa * __uint_as_float(o[e + 1]) + wb * y.y);
+            o[e + 2] = __float_as_uint(wa * __uint_as_float(o[e + 2]) + wb * y.z);
+            o[e + 3] = __float_as_uint(wa * __uint_as_float(o[e + 3]) + wb * y.w);
+          }
+          if (valid) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) st_global_v8(dst + cc * 32 + e, o + e);
           }
         }
-        p.pre_ml[at * kSpRows + r] = make_float2(M, wa * l + wb * other.y);
+        if (valid) p.rec_ml[at] = make_float2(M, wa * l + wb * other.y);
       }
     }
-    // records of this part that no tile fell into
-    if (g == 0 || !alternate)
-      for (int i = rec + 1; i < p.part_records; ++i) p.pre_ml[record_at(i) * kSpRows + r] = make_float2(-INFINITY, 0.f);
     tc_fence_before_sync();
   }
   __syncthreads();
@@ -1104,10 +1097,10 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 3 : 2)
     for (int c = 0; c < 2; ++c) {
       const int n = nt * 8 + 2 * qd + c;
       if (n >= p.group) continue;
-      const int64_t at = (static_cast<int64_t>(part) * p.num_seqs + s) * p.num_q_heads + h * p.group + n;
-      float *dst = p.suf_o + at * D;
+      const int64_t at = (static_cast<int64_t>(p.prefix_parts + part) * p.num_seqs + s) * p.num_q_heads + h * p.group + n;
+      float *dst = p.rec_o + at * D;
       if (gq == 0)  // weights of E4M3 tiles are 2^(z - m + 8)
-        p.suf_ml[at] = make_float2(ws.m[nt][c] - (FP8 ? kSpF16Log2 : 0.f), ws.l[nt][c]);
+        p.rec_ml[at] = make_float2(ws.m[nt][c] - (FP8 ? kSpF16Log2 : 0.f), ws.l[nt][c]);
 #pragma unroll
       for (int mt = 0; mt < KS; ++mt) {
         const int d0 = FP8 ? 16 * mt + 2 * gq : 16 * mt + gq, d1 = FP8 ? d0 + 1 : d0 + 8;
@@ -1119,107 +1112,69 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 3 : 2)
 
 // ------------------------------------------------------------------- join
 
-// 32 rows (sequence, head of KV head h) and 32 of their elements a CTA:
-//     out = out_scale sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i
-// over a row's prefix records and its own parts. First a thread takes one
-// 16-byte chunk of a row of the prefix records as they lie (a warp reads one
-// chunk of 32 rows, whole lines), then, through shared memory, a warp takes
-// a row. Small CTAs: the records of a few thousand rows fill the GPU's loads.
-constexpr int kJoinRows = 32;
-constexpr int kJoinCols = 32;
+// One warp a row (sequence, query head), its prefix records and its own parts:
+//     out = out_scale sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i,
+// kJoinBatch records in flight, M the maximum so far.
+constexpr int kJoinBatch = 4;
 
 template <int D>
 __global__ void __launch_bounds__(256) shared_join_kernel(const SharedParams p) {
-  constexpr int U = 4;  // records in flight
-  __shared__ float s_o[kJoinRows][kJoinCols + 4];
-  __shared__ float2 s_ml[kJoinRows];
-  __shared__ int s_parts[kJoinRows];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int h = blockIdx.y, all = p.num_seqs * p.group;
-  const int idx = blockIdx.x * kJoinRows + lane;  // this lane's row
-  SharedRow r{};
-  if (idx < all) r = shared_row(p, idx / p.group);
+  constexpr int V = D / 32;
+  const int lane = threadIdx.x & 31;
+  const int64_t rows = static_cast<int64_t>(p.num_seqs) * p.num_q_heads;
+  const int64_t w = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (w >= rows) return;
+  const SharedRow r = shared_row(p, static_cast<int>(w / p.num_q_heads));
+  const int n = r.prefix_parts + r.own_parts;
   wait_for_primary();
-  // all records of the row's parts; unused ones are empty
-  const int records = r.prefix_parts * p.part_records;
-  const int64_t stride = static_cast<int64_t>(p.num_kv_heads) * (2 * p.row_tiles) * kSpRows;
-  int64_t at = 0;
-  if (records > 0) {
-    const int s = idx / p.group;
-    // groups that overlap leave places unwritten: kept inside the records
-    const int slot = min(max(p.row_of[s], 0), 2 * p.row_tiles * p.tokens_per_tile - 1);
-    const int tile = slot / p.tokens_per_tile;
-    at = (static_cast<int64_t>(h) * (2 * p.row_tiles) + tile) * kSpRows + (slot - tile * p.tokens_per_tile) * p.group +
-         (idx - s * p.group);
-  }
-  const float2 *pre_ml = p.pre_ml + at;
-  // rows are the fastest index of a chunk: record i's chunk c of tile-row `at`
-  const float4 *pre_o = reinterpret_cast<const float4 *>(p.pre_o) + (at / kSpRows * (D / 4) + blockIdx.z * 8 + warp) * kSpRows +
-                        at % kSpRows;
-  float M = -INFINITY, l = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i0 = 0; i0 < records; i0 += U) {
-    float2 ml[U];
-    float4 x[U];
+  float acc[V], M = -INFINITY, l = 0.f;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      ml[u] = make_float2(-INFINITY, 0.f);
-      x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (i0 + u < records) {
-        ml[u] = pre_ml[(i0 + u) * stride];
-        x[u] = pre_o[(i0 + u) * stride * (D / 4)];
+  for (int v = 0; v < V; ++v) acc[v] = 0.f;
+  for (int i0 = 0; i0 < n; i0 += kJoinBatch) {
+    float2 ml[kJoinBatch];
+    float x[kJoinBatch][V];
+#pragma unroll
+    for (int u = 0; u < kJoinBatch; ++u) {
+      const int i = min(i0 + u, n - 1);
+      const int64_t at = (i < r.prefix_parts ? i : p.prefix_parts + i - r.prefix_parts) * rows + w;
+      ml[u] = p.rec_ml[at];
+      const float *o = p.rec_o + at * D + lane * V;
+      if constexpr (V == 4) {
+        const float4 y = *reinterpret_cast<const float4 *>(o);
+        x[u][0] = y.x;
+        x[u][1] = y.y;
+        x[u][2] = y.z;
+        x[u][3] = y.w;
+      } else {
+        const float2 y = *reinterpret_cast<const float2 *>(o);
+        x[u][0] = y.x;
+        x[u][1] = y.y;
       }
     }
     float top = M;
 #pragma unroll
-    for (int u = 0; u < U; ++u) top = fmaxf(top, ml[u].x);
+    for (int u = 0; u < kJoinBatch; ++u) top = fmaxf(top, ml[u].x);
     const float a = M == -INFINITY ? 0.f : exp2f(M - top);
-    l *= a;
-    acc.x *= a;
-    acc.y *= a;
-    acc.z *= a;
-    acc.w *= a;
     M = top;
+    l *= a;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (ml[u].x == -INFINITY) continue;  // an empty record holds no o
-      const float w = exp2f(ml[u].x - M);
-      l += w * ml[u].y;
-      acc.x += w * x[u].x;
-      acc.y += w * x[u].y;
-      acc.z += w * x[u].z;
-      acc.w += w * x[u].w;
+    for (int v = 0; v < V; ++v) acc[v] *= a;
+#pragma unroll
+    for (int u = 0; u < kJoinBatch; ++u) {
+      if (i0 + u >= n || ml[u].x == -INFINITY) continue;
+      const float wt = exp2f(ml[u].x - M);
+      l += wt * ml[u].y;
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[v] += wt * x[u][v];
     }
   }
-  *reinterpret_cast<float4 *>(&s_o[lane][4 * warp]) = acc;
-  if (warp == 0) {
-    s_ml[lane] = make_float2(M, l);
-    s_parts[lane] = idx < all ? r.own_parts + (records > 0 ? 65536 : 0) : -1;
-  }
-  __syncthreads();
-  const int64_t rows = static_cast<int64_t>(p.num_seqs) * p.num_q_heads;
+  float *out = p.out + w * D + lane * V;
 #pragma unroll
-  for (int k = warp; k < kJoinRows; k += 8) {
-    const int parts = s_parts[k] & 65535;
-    if (s_parts[k] < 0) continue;
-    const int i0 = blockIdx.x * kJoinRows + k, s = i0 / p.group;
-    const int64_t row = static_cast<int64_t>(s) * p.num_q_heads + h * p.group + (i0 - s * p.group);
-    const float2 pre = s_ml[k];
-    float top = pre.x, sum = pre.y, x = s_o[k][lane];
-    const float *o = p.suf_o + row * D + blockIdx.z * kJoinCols + lane;
-#pragma unroll 4
-    for (int i = 0; i < parts; ++i) {
-      const float2 ml = p.suf_ml[i * rows + row];
-      const float y = o[i * rows * D];
-      const float t = fmaxf(top, ml.x);
-      const float a = top == -INFINITY ? 0.f : exp2f(top - t), w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - t);
-      top = t;
-      sum = sum * a + w * ml.y;
-      x = x * a + w * y;
-    }
-    // no token at all: zeros
-    p.out[row * D + blockIdx.z * kJoinCols + lane] = s_parts[k] > 0 ? x / sum * p.out_scale : 0.f;
-  }
+  for (int v = 0; v < V; ++v) acc[v] = n > 0 ? acc[v] / l * p.out_scale : 0.f;  // no token: zeros
+  if constexpr (V == 4)
+    *reinterpret_cast<float4 *>(out) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+  else
+    *reinterpret_cast<float2 *>(out) = make_float2(acc[0], acc[1]);
 }
 
 }  // namespace pa
