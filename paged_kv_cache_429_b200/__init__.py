@@ -140,6 +140,14 @@ def _call(what: str, dev: int, *args) -> None:
         raise PagedAttentionError(rc, what)
 
 
+def _status(rc, what: str) -> bool:
+    """Whether a call of the extension was made: None is a call that it does
+    not take and leaves to the long way."""
+    if rc:
+        raise PagedAttentionError(rc, what)
+    return rc is not None
+
+
 def _raw_stream(stream: Optional[torch.cuda.Stream], dev: int) -> int:
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
@@ -297,6 +305,13 @@ def pa_decode_shared_prefix(out: torch.Tensor, q: torch.Tensor, k_cache: torch.T
     sequence's prefix (default: max_context_len); a tight bound keeps the
     suffix launch small. Without a workspace one is allocated with torch for
     this call."""
+    if workspace is None and stream is None and _status(
+            (_lib._ext or _lib.binding()).decode_shared_prefix(
+                out, q, k_cache, v_cache, block_tables, context_lens, max_context_len, group_start,
+                prefix_blocks, max_prefix_blocks,
+                max_context_len if max_suffix_len is None else max_suffix_len, sm_scale, k_scale,
+                v_scale), "pa_decode_shared_prefix"):
+        return out
     dev = _check_all((out, q, k_cache, v_cache, block_tables, context_lens, group_start,
                       prefix_blocks), _SHARED_SPECS)
     S, Hq, D = q.shape
@@ -443,6 +458,11 @@ def pa_rope_and_cache(q_out: torch.Tensor, q: torch.Tensor, key: torch.Tensor,
     their slots of the caches. q, key, value may be views with a token
     stride; the rotated part of a head is its first 2 * len(inv_freq)
     elements."""
+    if stream is None and _status(
+            (_lib._ext or _lib.binding()).rope_and_cache(
+                q_out, q, key, value, k_cache, v_cache, slot_mapping, positions, inv_freq,
+                interleaved, rope_scale, k_scale, v_scale), "pa_rope_and_cache"):
+        return q_out
     for t, name in ((q, "q"), (key, "key"), (value, "value")):
         _need_rows(t, name)
     dev = _check_all((q_out, k_cache, v_cache, slot_mapping, positions, inv_freq), _ROPE_SPECS)
@@ -482,6 +502,12 @@ def pa_extend_tables(block_tables: torch.Tensor, context_lens: torch.Tensor,
     stack into block_tables [S][W], the new lengths and count (in place if
     the same tensors are given), slots, positions and query_start of the
     tokens. num_blocks: the pool's size (default: free_blocks' length)."""
+    if stream is None and _status(
+            (_lib._ext or _lib.binding()).extend_tables(
+                block_tables, context_lens, new_lens, free_blocks, free_count, context_lens_out,
+                free_count_out, slot_mapping, positions, query_start,
+                -1 if num_blocks is None else num_blocks), "pa_extend_tables"):
+        return
     dev = _check_all((block_tables, context_lens, new_lens, free_blocks, free_count,
                       context_lens_out, free_count_out, slot_mapping, positions, query_start),
                      _EXTEND_SPECS)
@@ -517,6 +543,12 @@ def pa_release_tables(block_tables: torch.Tensor, context_lens: torch.Tensor,
     """Push the blocks of the rows with release != 0, behind their first
     keep_blocks, on the free stack (see pa.h); lengths and count as for
     pa_extend_tables."""
+    if stream is None and _status(
+            (_lib._ext or _lib.binding()).release_tables(
+                block_tables, context_lens, release, free_blocks, free_count, context_lens_out,
+                free_count_out, keep_blocks, -1 if num_blocks is None else num_blocks),
+            "pa_release_tables"):
+        return
     dev = _check_all((block_tables, context_lens, release, free_blocks, free_count,
                       context_lens_out, free_count_out), _RELEASE_SPECS)
     S, W = block_tables.shape

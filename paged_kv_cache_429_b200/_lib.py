@@ -98,3 +98,21 @@ def lib() -> ctypes.CDLL:
         fn.argtypes = args
     _lib = handle
     return handle
+
+
+_ext = None
+
+
+def binding():
+    """The loaded extension of csrc/binding.cpp (the short way into lib())."""
+    global _ext
+    if _ext is None:
+        lib()
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise LibraryNotBuilt(
+                f"the _binding extension is missing or does not load ({e}): build it with "
+                "`python -m paged_kv_cache_429_b200.build` (no fallback exists)") from e
+        _ext = _binding
+    return _ext

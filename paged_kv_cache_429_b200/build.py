@@ -1,4 +1,5 @@
-"""Build libpa.so (CUDA kernels + C ABI + host block pool) for sm_100a.
+"""Build libpa.so (CUDA kernels + C ABI + host block pool) for sm_100a, and
+_binding, the Python extension in front of it (csrc/binding.cpp).
 
 Usage: ``python -m paged_kv_cache_429_b200.build`` (or via
 ``__graft_entry__.build()``). The library is written next to this file so it
@@ -9,6 +10,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -20,6 +22,10 @@ SOURCES = [os.path.join(CSRC, "pa_api.cu"), os.path.join(CSRC, "pa_noalloc.cu"),
            os.path.join(CSRC, "pool.cpp")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC)
                   if f.endswith((".cuh", ".h"))] + [os.path.join(INCLUDE, "pa.h")]
+
+BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
+BINDING = os.path.join(HERE, "_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
+BINDING_DEPS = [BINDING_SOURCE, os.path.join(INCLUDE, "pa.h")]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -34,21 +40,47 @@ def _nvcc() -> str:
     return cand if os.path.exists(cand) else "nvcc"
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+def _newer(target: str, deps) -> bool:
+    if not os.path.exists(target):
         return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(f) <= t for f in DEPS)
+    t = os.path.getmtime(target)
+    return all(os.path.getmtime(f) <= t for f in deps)
+
+
+def up_to_date() -> bool:
+    return _newer(LIB, DEPS)
+
+
+def build_binding(force: bool = False) -> str:
+    """The extension links libpa.so next to it, and the torch it is run with."""
+    if not force and _newer(BINDING, BINDING_DEPS):
+        return BINDING
+    import torch
+    troot = os.path.dirname(torch.__file__)
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    include = [INCLUDE, sysconfig.get_paths()["include"], os.path.join(troot, "include"),
+               os.path.join(troot, "include", "torch", "csrc", "api", "include"),
+               os.path.join(cuda, "include")]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    for d in include:
+        cmd += ["-isystem" if d is not INCLUDE else "-I", d]
+    cmd += ["-o", BINDING, BINDING_SOURCE, "-L", HERE, "-lpa", "-L", os.path.join(troot, "lib"),
+            "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+    subprocess.run(cmd, check=True)
+    return BINDING
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
+        build_binding()
         return LIB
     cmd = [_nvcc(), *NVCC_FLAGS, "-I", INCLUDE, "-I", CSRC, "-o", LIB, *SOURCES]
     if verbose:
         cmd.insert(1, "-Xptxas=-v")
         print(" ".join(cmd), file=sys.stderr)
     subprocess.run(cmd, check=True)
+    build_binding(force)
     return LIB
 
 
