@@ -321,9 +321,9 @@ pa_status launch_shared(const pa::SharedParams &p, const void *k_cache, const vo
 template <int D, bool FP8>
 pa_status launch_rope(pa::RopeParams p, bool interleaved, cudaStream_t st, int dev) {
   // Few tokens: one a CTA and its units cut into slices of one a thread, so
-  // that a decode step fills the GPU; from four tokens an SM on, a CTA takes
+  // that a decode step fills the GPU; from 16 tokens an SM on, a CTA takes
   // four tokens whole and their angles are formed once.
-  const bool few = p.num_tokens < 4 * device_sm_count(dev);
+  const bool few = p.num_tokens < 16 * device_sm_count(dev);
   p.tokens_per_cta = few ? 1 : pa::kRopeTokens;
   const int units = p.tokens_per_cta * (p.num_q_heads + 2 * p.num_kv_heads) * (D / 16);
   p.units_per_cta = few ? pa::kRopeThreads : units;
@@ -337,14 +337,21 @@ pa_status launch_rope(pa::RopeParams p, bool interleaved, cudaStream_t st, int d
   return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
-// One phase of a table kernel over `ctas` CTAs, with `ints` integers of
-// dynamic shared memory (at most max_ints for any call).
+// One phase of a table kernel, with `ints` integers of dynamic shared memory
+// (at most max_ints for any call).
 template <typename Params>
-pa_status launch_table_kernel(void (*kern)(Params), const Params &p, int64_t ctas, size_t ints, size_t max_ints,
-                              std::atomic<uint64_t> &attr_done, cudaStream_t st, int dev) {
+pa_status launch_table_kernel(void (*kern)(Params), const Params &p, int64_t ctas, int threads, size_t ints,
+                              size_t max_ints, std::atomic<uint64_t> &attr_done, cudaStream_t st, int dev) {
   if (!ensure_smem_attr(kern, max_ints * sizeof(int32_t), attr_done, dev)) return PA_ERR_CUDA;
-  kern<<<static_cast<unsigned>(ctas), pa::kTabThreads, ints * sizeof(int32_t), st>>>(p);
+  kern<<<static_cast<unsigned>(ctas), threads, ints * sizeof(int32_t), st>>>(p);
   return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+// Threads of a one-CTA call: as many as its rows, or its tokens four a
+// thread, keep busy (a small CTA starts and synchronises sooner).
+int table_threads(int64_t rows, int64_t items) {
+  const int64_t want = std::max(rows, (items + pa::kTabBatch - 1) / pa::kTabBatch);
+  return static_cast<int>(std::min<int64_t>(std::max<int64_t>((want + 31) / 32 * 32, 64), pa::kTabThreads));
 }
 
 }  // namespace
@@ -904,20 +911,21 @@ pa_status pa_extend_tables(int32_t *block_tables, int max_blocks_per_seq, const 
   p.num_blocks = num_blocks;
   p.free_capacity = free_capacity;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  p.wide = aligned(slot_mapping, 16) && aligned(positions, 16);
+  p.wide = aligned(slot_mapping, 32) && aligned(positions, 16);
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return PA_ERR_CUDA;
   using pa::TablePhase;
   const size_t ints = 3 * static_cast<size_t>(num_seqs) + 1, most = 3 * pa::kTabMaxSeqs + 1;
-  static std::atomic<uint64_t> attr_all{0}, attr_work{0}, attr_finish{0};
+  static std::atomic<uint64_t> attr_all{0}, attr_work{0};
   if (num_tokens <= pa::kTabSmallTokens)
-    return launch_table_kernel(pa::extend_kernel<TablePhase::kAll>, p, 1, ints, most, attr_all, st, dev);
+    return launch_table_kernel(pa::extend_kernel<TablePhase::kAll>, p, 1, table_threads(num_seqs, num_tokens), ints, most,
+                               attr_all, st, dev);
   const int64_t ctas = std::min<int64_t>((static_cast<int64_t>(num_tokens) + pa::kTabPerCta - 1) / pa::kTabPerCta,
                                          device_sm_count(dev));
   const pa_status rc =
-      launch_table_kernel(pa::extend_kernel<TablePhase::kWork>, p, ctas, ints, most, attr_work, st, dev);
+      launch_table_kernel(pa::extend_kernel<TablePhase::kWork>, p, ctas, pa::kTabThreads, ints, most, attr_work, st, dev);
   if (rc != PA_OK) return rc;
-  return launch_table_kernel(pa::extend_kernel<TablePhase::kFinish>, p, 1, 0, most, attr_finish, st, dev);
+  return launch_beside(pa::extend_kernel<TablePhase::kFinish>, dim3(1), pa::kTabThreads, 0, st, p);
 }
 
 pa_status pa_release_tables(const int32_t *block_tables, int max_blocks_per_seq,
@@ -954,15 +962,16 @@ pa_status pa_release_tables(const int32_t *block_tables, int max_blocks_per_seq,
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return PA_ERR_CUDA;
   using pa::TablePhase;
-  static std::atomic<uint64_t> attr_all{0}, attr_work{0}, attr_finish{0};
+  static std::atomic<uint64_t> attr_all{0}, attr_work{0};
   const int64_t pushes = static_cast<int64_t>(num_seqs) * std::max(max_blocks_per_seq - keep_blocks, 0);  // at most
   if (pushes <= pa::kTabSmallBlocks)
-    return launch_table_kernel(pa::release_kernel<TablePhase::kAll>, p, 1, num_seqs, pa::kTabMaxSeqs, attr_all, st, dev);
+    return launch_table_kernel(pa::release_kernel<TablePhase::kAll>, p, 1, table_threads(num_seqs, pushes / 8), num_seqs,
+                               pa::kTabMaxSeqs, attr_all, st, dev);
   const int64_t ctas = std::min<int64_t>((pushes + pa::kTabPerCta - 1) / pa::kTabPerCta, device_sm_count(dev));
-  const pa_status rc = launch_table_kernel(pa::release_kernel<TablePhase::kWork>, p, ctas, num_seqs, pa::kTabMaxSeqs,
-                                           attr_work, st, dev);
+  const pa_status rc = launch_table_kernel(pa::release_kernel<TablePhase::kWork>, p, ctas, pa::kTabThreads, num_seqs,
+                                           pa::kTabMaxSeqs, attr_work, st, dev);
   if (rc != PA_OK) return rc;
-  return launch_table_kernel(pa::release_kernel<TablePhase::kFinish>, p, 1, 0, pa::kTabMaxSeqs, attr_finish, st, dev);
+  return launch_beside(pa::release_kernel<TablePhase::kFinish>, dim3(1), pa::kTabThreads, 0, st, p);
 }
 
 pa_status pa_copy_blocks(void *k_cache, void *v_cache, const int64_t *block_pairs, int num_pairs,

@@ -29,9 +29,9 @@
 
 namespace pa {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;
 constexpr int kRopeTokens = 4;     // most tokens of a CTA
-constexpr int kRopeBatch = 2;      // units of a thread in flight
+constexpr int kRopeBatch = 3;      // units of a thread in flight
 constexpr int kRopeMaxPairs = 64;  // rotary_dim <= 128
 
 struct RopeParams {

@@ -27,6 +27,7 @@
 
 #include "decode.cuh"
 #include "prefill.cuh"
+#include "ptx_step.cuh"
 
 namespace pa {
 
@@ -137,12 +138,6 @@ __device__ __forceinline__ SharedRow shared_row(const SharedParams &p, int s) {
   return r;
 }
 
-// Programmatic dependent launch: let the next kernel of the stream start
-// beside this one, and wait until the one before has finished (its writes
-// visible). Without the launch attribute neither does anything.
-__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // ------------------------------------------------------------ prefix parts
 
 constexpr int kSpSoftmaxWarps = 8;  // two warpgroups
@@ -191,13 +186,6 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "r"(addr));
   return v;
-}
-
-// 32 bytes, a whole sector, of one thread (32-byte aligned).
-__device__ __forceinline__ void st_global_v8(float *p, const uint32_t *v) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
 }
 
 // Byte of 16-byte chunk c (0..7) of row r in one 64-element half of an

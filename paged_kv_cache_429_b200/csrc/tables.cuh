@@ -26,13 +26,14 @@
 #pragma once
 
 #include "decode.cuh"
+#include "ptx_step.cuh"
 
 namespace pa {
 
 constexpr int kTabThreads = 1024;
 constexpr int kTabMaxSeqs = 16384;        // rows whose sums one CTA's shared memory holds
 constexpr int kTabBatch = 4;              // tokens or blocks of a thread in flight
-constexpr int kTabPerCta = kTabThreads * kTabBatch;
+constexpr int kTabPerCta = kTabThreads * kTabBatch;   // of a CTA of kTabThreads
 constexpr int kTabSmallTokens = 2 * kTabPerCta;   // extend: one CTA up to here
 constexpr int kTabSmallBlocks = 8 * kTabPerCta;   // release: one CTA up to this bound of its pushes
 
@@ -66,7 +67,7 @@ __device__ __forceinline__ Two block_exclusive_sum(Two v, Two &total) {
   if (lane == 31) s_warp[warp] = x;
   __syncthreads();
   if (warp == 0) {
-    Two w = s_warp[lane];
+    Two w = lane < blockDim.x / 32 ? s_warp[lane] : Two{0, 0};
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t a = __shfl_up_sync(0xffffffffu, w.a, o), b = __shfl_up_sync(0xffffffffu, w.b, o);
@@ -78,7 +79,7 @@ __device__ __forceinline__ Two block_exclusive_sum(Two v, Two &total) {
     s_warp[lane] = w;
   }
   __syncthreads();
-  total = s_warp[kTabThreads / 32 - 1];
+  total = s_warp[blockDim.x / 32 - 1];
   const Two before = warp ? s_warp[warp - 1] : Two{0, 0};
   return Two{before.a + x.a - v.a, before.b + x.b - v.b};
 }
@@ -115,7 +116,7 @@ struct ExtendParams {
   int num_tokens;
   int num_blocks;               // pool size: ids are checked against it
   int free_capacity;
-  bool wide;                    // slot_mapping and positions are 16-byte aligned
+  bool wide;                    // slot_mapping is 32-byte, positions 16-byte aligned
 };
 
 template <TablePhase PHASE>
@@ -125,7 +126,7 @@ __global__ void __launch_bounds__(kTabThreads) extend_kernel(const ExtendParams 
   int32_t *s_query = s_rows;           // [S + 1] tokens of earlier rows
   int32_t *s_first = s_query + S + 1;  // [S] blocks needed by earlier rows
   int32_t *s_len = s_first + S;        // [S]
-  const int per = (S + kTabThreads - 1) / kTabThreads;
+  const int per = (S + blockDim.x - 1) / blockDim.x;
   const int s0 = min(S, static_cast<int>(threadIdx.x) * per), s1 = min(S, s0 + per);
   const int64_t row_cap = static_cast<int64_t>(p.max_blocks_per_seq) * kBS;
   const int count = *p.free_count;
@@ -168,52 +169,71 @@ __global__ void __launch_bounds__(kTabThreads) extend_kernel(const ExtendParams 
     }
     __syncthreads();
     bool bad_id = false;
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * kTabPerCta;
-    for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kTabThreads + threadIdx.x) * kTabBatch;
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x * kTabBatch;
+    for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) * kTabBatch;
          t0 < p.num_tokens; t0 += stride) {
-      // four consecutive tokens: their rows (mostly one), then their block
-      // ids, then the stores
-      int t[kTabBatch], s[kTabBatch], pos[kTabBatch], id[kTabBatch];
-      int64_t slot[kTabBatch];
-#pragma unroll
-      for (int i = 0; i < kTabBatch; ++i) t[i] = static_cast<int>(min(t0 + i, static_cast<int64_t>(max(tokens - 1, 0))));
-      if (t0 < tokens) {
-        const int v[1] = {t[0]};
-        int k[1];
-        last_not_above(s_query, S, v, k);
-        if (t[kTabBatch - 1] < s_query[k[0] + 1]) {
-#pragma unroll
-          for (int i = 0; i < kTabBatch; ++i) s[i] = k[0];
-        } else {
-          last_not_above(s_query, S, t, s);
-        }
-      }
+      // four consecutive tokens: their rows, then their block ids, then the stores
+      int pos[kTabBatch], id[kTabBatch];
 #pragma unroll
       for (int i = 0; i < kTabBatch; ++i) {
         pos[i] = 0;
         id[i] = -1;
-        if (t0 + i < tokens) {
-          const int L = s_len[s[i]], old = (L + kBS - 1) / kBS;
-          pos[i] = L + t[i] - s_query[s[i]];
-          const int j = pos[i] / kBS;
-          int32_t *entry = p.block_tables + static_cast<int64_t>(s[i]) * p.max_blocks_per_seq + j;
-          if (j < old) {
-            id[i] = *entry;
-          } else {
-            id[i] = p.free_blocks[count - 1 - (s_first[s[i]] + j - old)];
-            if (pos[i] % kBS == 0) *entry = id[i];  // a new block begins with a new token
-          }
+      }
+      const int live = static_cast<int>(min(static_cast<int64_t>(kTabBatch), tokens - t0));  // <= 0: padding
+      // the id of block j of row s, from its table or the stack; a new
+      // block's entry is written by the thread of its first token
+      auto block_id = [&](int s, int j, int old, bool starts) {
+        int32_t *entry = p.block_tables + static_cast<int64_t>(s) * p.max_blocks_per_seq + j;
+        if (j < old) return *entry;
+        const int b = p.free_blocks[count - 1 - (s_first[s] + j - old)];
+        if (starts) *entry = b;
+        return b;
+      };
+      if (live > 0) {
+        const int v[1] = {static_cast<int>(t0)};
+        int k[1] = {-1};
+        // rows of few tokens are looked up one token at a time
+        if (p.num_tokens > kTabBatch * S) last_not_above(s_query, S, v, k);
+        if (k[0] >= 0 && v[0] + live <= s_query[k[0] + 1]) {  // one row: its positions follow one another, in two blocks at most
+          const int s = k[0], L = s_len[s], old = (L + kBS - 1) / kBS;
+          const int p0 = L + v[0] - s_query[s], off = p0 % kBS, next = (p0 + live - 1) / kBS;
+          const int id0 = block_id(s, p0 / kBS, old, off == 0);
+          const int id1 = next != p0 / kBS ? block_id(s, next, old, true) : id0;
+#pragma unroll
+          for (int i = 0; i < kTabBatch; ++i)
+            if (i < live) {
+              pos[i] = p0 + i;
+              id[i] = off + i < kBS ? id0 : id1;
+            }
+        } else {
+          int t[kTabBatch], s[kTabBatch];
+#pragma unroll
+          for (int i = 0; i < kTabBatch; ++i) t[i] = v[0] + min(i, live - 1);
+          last_not_above(s_query, S, t, s);
+#pragma unroll
+          for (int i = 0; i < kTabBatch; ++i)
+            if (i < live) {
+              const int L = s_len[s[i]];
+              pos[i] = L + t[i] - s_query[s[i]];
+              id[i] = block_id(s[i], pos[i] / kBS, (L + kBS - 1) / kBS, pos[i] % kBS == 0);
+            }
         }
       }
+      int64_t slot[kTabBatch];
 #pragma unroll
       for (int i = 0; i < kTabBatch; ++i) {
         const bool in_pool = id[i] >= 0 && id[i] < p.num_blocks;
-        bad_id |= t0 + i < tokens && !in_pool;
+        bad_id |= i < live && !in_pool;
         slot[i] = in_pool ? static_cast<int64_t>(id[i]) * kBS + pos[i] % kBS : -1;
       }
-      if (p.wide && t0 + kTabBatch <= p.num_tokens) {  // 16-byte stores
-        *reinterpret_cast<longlong2 *>(p.slot_mapping + t0) = make_longlong2(slot[0], slot[1]);
-        *reinterpret_cast<longlong2 *>(p.slot_mapping + t0 + 2) = make_longlong2(slot[2], slot[3]);
+      if (p.wide && t0 + kTabBatch <= p.num_tokens) {  // whole sectors
+        uint32_t w[2 * kTabBatch];
+#pragma unroll
+        for (int i = 0; i < kTabBatch; ++i) {
+          w[2 * i] = static_cast<uint32_t>(slot[i]);
+          w[2 * i + 1] = static_cast<uint32_t>(slot[i] >> 32);
+        }
+        st_global_v8(p.slot_mapping + t0, w);
         *reinterpret_cast<int4 *>(p.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
       } else {
 #pragma unroll
@@ -228,6 +248,7 @@ __global__ void __launch_bounds__(kTabThreads) extend_kernel(const ExtendParams 
   }
   if (PHASE != TablePhase::kWork) {
     if (PHASE == TablePhase::kAll) __syncthreads();
+    if (PHASE == TablePhase::kFinish) wait_for_primary();
     for (int s = s0; s < s1; ++s)  // the rows this thread alone has read
       p.context_lens_out[s] = p.context_lens[s] + (ok ? p.new_lens[s] : 0);
     if (threadIdx.x == 0) *p.free_count_out = count - (ok ? static_cast<int>(total.b) : 0);
@@ -261,7 +282,7 @@ template <TablePhase PHASE>
 __global__ void __launch_bounds__(kTabThreads) release_kernel(const ReleaseParams p) {
   extern __shared__ int32_t s_first[];  // [S] blocks pushed by earlier rows
   const int S = p.num_seqs;
-  const int per = (S + kTabThreads - 1) / kTabThreads;
+  const int per = (S + blockDim.x - 1) / blockDim.x;
   const int s0 = min(S, static_cast<int>(threadIdx.x) * per), s1 = min(S, s0 + per);
   const int count = *p.free_count;
   Two mine{0, 0};
@@ -285,9 +306,9 @@ __global__ void __launch_bounds__(kTabThreads) release_kernel(const ReleaseParam
       b += released_blocks(p, s);
     }
     __syncthreads();
-    const int stride = gridDim.x * kTabThreads;
+    const int stride = gridDim.x * blockDim.x;
     bool bad_id = false;
-    for (int64_t k0 = blockIdx.x * kTabThreads + threadIdx.x; k0 < blocks; k0 += kTabBatch * stride) {
+    for (int64_t k0 = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; k0 < blocks; k0 += kTabBatch * stride) {
       int k[kTabBatch], s[kTabBatch], id[kTabBatch];
 #pragma unroll
       for (int i = 0; i < kTabBatch; ++i) k[i] = static_cast<int>(min(k0 + i * stride, static_cast<int64_t>(blocks - 1)));
@@ -308,6 +329,7 @@ __global__ void __launch_bounds__(kTabThreads) release_kernel(const ReleaseParam
     if (!ok && threadIdx.x == 0)
       raise_error((length_bad ? kErrLengthRange : 0u) | (count_bad ? kErrFreeRange : 0u));
     if (PHASE == TablePhase::kAll) __syncthreads();
+    if (PHASE == TablePhase::kFinish) wait_for_primary();
     for (int s = s0; s < s1; ++s) {  // the rows this thread alone has read
       const int64_t L = p.context_lens[s];
       p.context_lens_out[s] = static_cast<int>(
