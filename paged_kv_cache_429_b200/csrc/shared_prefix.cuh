@@ -277,6 +277,10 @@ __global__ void __launch_bounds__(SpPlan<D, FP8>::kThreads, 1)
   const bool alternate = nseq <= tpt;
   const int my_tiles0 = alternate ? (nt + 1) / 2 : nt, my_tiles1 = alternate ? nt / 2 : nt;
 
+  // the producers' first table entries, on their way during the set-up
+  const int32_t *bt = p.block_tables + static_cast<int64_t>(first) * p.max_blocks_per_seq + blk0;
+  int first_ids = -1;
+  if ((warp == kKWarp || warp == kVWarp) && lane < nblk) first_ids = bt[lane];
   if (threadIdx.x == 0) {
     for (int g = 0; g < 2; ++g) {
       mbar_init(bar_q + 8u * g, 1);
@@ -334,14 +338,13 @@ __global__ void __launch_bounds__(SpPlan<D, FP8>::kThreads, 1)
           }
         }
       }
-      const int32_t *bt = p.block_tables + static_cast<int64_t>(first) * p.max_blocks_per_seq + blk0;
       const int total_rows = p.num_blocks * p.num_kv_heads * kBS;
       bool ok = true, bad_id = false;
       int issued = 0, mine = -1;
       for (int j = 0; j < nt && ok; ++j) {
         if ((j & 3) == 0) {  // 32 table entries, four tiles, a load
           const int jb = j * kSpBlocks + lane;
-          mine = jb < nblk ? bt[jb] : -1;
+          mine = j == 0 ? first_ids : (jb < nblk ? bt[jb] : -1);
         }
         int phys[kSpBlocks];
 #pragma unroll
@@ -491,21 +494,30 @@ __global__ void __launch_bounds__(SpPlan<D, FP8>::kThreads, 1)
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(PL::kConvertRegs));
       const int c = threadIdx.x - kSpSoftmaxWarps * 32;
       bool ok = true;
-      // 16 codes a step: eight neighbouring lanes take four chunks of two
-      // rows, whose f16 chunks then fall into different banks
+      // A thread takes chunk c & 3 (16 codes) of rows c / 4, c / 4 + 32, ... of
+      // each 64-element half: eight neighbouring lanes then hold four chunks
+      // of two rows, whose f16 chunks fall into different banks, and a row's
+      // place under the swizzle is the same in every step.
+      const int ch = c & 3, row = c >> 2;
+      const uint32_t from = swz<D, true>(row, ch * 16);
+      const uint32_t to0 = op_chunk(row, 2 * ch), to1 = op_chunk(row, 2 * ch + 1);
       auto widen = [&](uint32_t src, uint32_t dst) {
-#pragma unroll 4
-        for (int i = 0; i < D / 16; ++i) {
-          const int n = i * 128 + c;
-          const int ch = n & 3, row = (n >> 2) & 127, half = n >> 9;
-          const uint4 x = ld_shared_v4(src + swz<D, true>(row, half * 64 + ch * 16));
-          uint4 a, b;
-          e4m3x4_to_f16x2x2(x.x, a.x, a.y);
-          e4m3x4_to_f16x2x2(x.y, a.z, a.w);
-          e4m3x4_to_f16x2x2(x.z, b.x, b.y);
-          e4m3x4_to_f16x2x2(x.w, b.z, b.w);
-          st_shared_v4(dst + half * PL::kHalfBytes + op_chunk(row, 2 * ch), a);
-          st_shared_v4(dst + half * PL::kHalfBytes + op_chunk(row, 2 * ch + 1), b);
+#pragma unroll
+        for (int half = 0; half < H; ++half) {
+          uint4 x[4];
+          // bytes 64 .. 127 of a row: chunk index + 4, under the swizzle chunk ^ 4
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[i] = ld_shared_v4(src + (from ^ (half * 64)) + i * 32 * D);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint4 a, b;
+            e4m3x4_to_f16x2x2(x[i].x, a.x, a.y);
+            e4m3x4_to_f16x2x2(x[i].y, a.z, a.w);
+            e4m3x4_to_f16x2x2(x[i].z, b.x, b.y);
+            e4m3x4_to_f16x2x2(x[i].w, b.z, b.w);
+            st_shared_v4(dst + half * PL::kHalfBytes + to0 + i * 32 * 128, a);
+            st_shared_v4(dst + half * PL::kHalfBytes + to1 + i * 32 * 128, b);
+          }
         }
         fence_proxy_async_smem();
       };
@@ -554,8 +566,8 @@ __global__ void __launch_bounds__(SpPlan<D, FP8>::kThreads, 1)
       }
       const uint32_t qrow = sq + (alternate ? 0 : g * PL::kTileBytes);
       float amax = 0.f;
-#pragma unroll 1
-      for (int c = 0; c < D / 8 && ok; ++c) {
+#pragma unroll 4
+      for (int c = 0; c < D / 8; ++c) {
         const uint4 x = ld_shared_v4(qrow + (c >> 3) * PL::kHalfBytes + op_chunk(r, c & 7));
         const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
@@ -573,8 +585,8 @@ __global__ void __launch_bounds__(SpPlan<D, FP8>::kThreads, 1)
       // every reader of the bf16 rows is done before they are overwritten
       if (alternate) named_bar_sync(3, 256);
       if (!alternate || g == 0) {
-#pragma unroll 1
-        for (int c = 0; c < D / 8 && ok; ++c) {
+#pragma unroll 4
+        for (int c = 0; c < D / 8; ++c) {
           const uint32_t at = qrow + (c >> 3) * PL::kHalfBytes + op_chunk(r, c & 7);
           uint4 x = ld_shared_v4(at);
           uint32_t *w = &x.x;
