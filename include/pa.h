@@ -423,8 +423,9 @@ PA_API pa_status pa_rope_and_cache(void *q_out, const void *q, const void *key,
  * (PA_DEVERR_LENGTH_RANGE) or a count outside [0, free_capacity]
  * (PA_DEVERR_FREE_RANGE) leave tables, lengths and count as they were, with
  * every slot -1, positions and query_start 0. A block id outside
- * [0, num_blocks) gives slot -1 (PA_DEVERR_BLOCK_RANGE). num_seqs up to 16384
- * (more: PA_ERR_UNSUPPORTED). Other pointers 4-byte aligned, slot_mapping 8. */
+ * [0, num_blocks) gives slot -1 (PA_DEVERR_BLOCK_RANGE). num_seqs up to 16384,
+ * max_blocks_per_seq below 2^27 (more: PA_ERR_UNSUPPORTED). Other pointers
+ * 4-byte aligned, slot_mapping 8. */
 PA_API pa_status pa_extend_tables(int32_t *block_tables, int max_blocks_per_seq,
                                   const int32_t *context_lens,
                                   const int32_t *new_lens,

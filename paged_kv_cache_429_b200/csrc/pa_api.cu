@@ -608,6 +608,7 @@ pa_status pa_decode_shared_prefix(float *out, const void *q, const void *k_cache
       !(std::isfinite(k_scale) && k_scale > 0.f && std::isfinite(v_scale) && v_scale > 0.f))
     return PA_ERR_INVALID_ARG;
   if (num_groups > 65535) return PA_ERR_UNSUPPORTED;
+  if (max_blocks_per_seq > INT32_MAX / pa::kBS) return PA_ERR_UNSUPPORTED;  // token counts are 32-bit
   if (num_seqs == 0) return PA_OK;
   if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens)
     return PA_ERR_INVALID_ARG;
@@ -883,7 +884,7 @@ pa_status pa_extend_tables(int32_t *block_tables, int max_blocks_per_seq, const 
   if (num_seqs < 0 || num_tokens < 0 || max_blocks_per_seq < 0 || free_capacity < 0 || num_blocks <= 0)
     return PA_ERR_INVALID_ARG;
   if (block_size != pa::kBS) return PA_ERR_UNSUPPORTED;
-  if (num_seqs > pa::kTabMaxSeqs) return PA_ERR_UNSUPPORTED;
+  if (num_seqs > pa::kTabMaxSeqs || max_blocks_per_seq > INT32_MAX / pa::kBS) return PA_ERR_UNSUPPORTED;
   if (!free_count || !free_count_out || !query_start) return PA_ERR_INVALID_ARG;
   if (free_capacity > 0 && !free_blocks) return PA_ERR_INVALID_ARG;
   if (num_seqs > 0 && (!context_lens || !new_lens || !context_lens_out)) return PA_ERR_INVALID_ARG;
@@ -936,7 +937,7 @@ pa_status pa_release_tables(const int32_t *block_tables, int max_blocks_per_seq,
   if (num_seqs < 0 || max_blocks_per_seq < 0 || free_capacity < 0 || keep_blocks < 0 || num_blocks <= 0)
     return PA_ERR_INVALID_ARG;
   if (block_size != pa::kBS) return PA_ERR_UNSUPPORTED;
-  if (num_seqs > pa::kTabMaxSeqs) return PA_ERR_UNSUPPORTED;
+  if (num_seqs > pa::kTabMaxSeqs || max_blocks_per_seq > INT32_MAX / pa::kBS) return PA_ERR_UNSUPPORTED;
   if (!free_count || !free_count_out) return PA_ERR_INVALID_ARG;
   if (free_capacity > 0 && !free_blocks) return PA_ERR_INVALID_ARG;
   if (num_seqs > 0 && (!context_lens || !release || !context_lens_out)) return PA_ERR_INVALID_ARG;

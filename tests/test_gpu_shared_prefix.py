@@ -71,6 +71,7 @@ class Batch:
         self.q = (torch.randn((S, hq, d), generator=g, device="cuda") * spread).to(torch.bfloat16)
         shape = (nb, hkv, B, d)
         self.vmax = 0.0
+        self.scale = d ** -0.5
 
         def cache(scale):
             x = torch.randn(shape, generator=g, device="cuda")
@@ -100,7 +101,7 @@ class Batch:
         a.update(kw)
         return pa_decode_shared_prefix(
             out, self.q if q is None else q, self.k, self.v, self.dev(a["tables"]), self.dev(a["lens"]), a["max_len"],
-            self.dev(a["start"]), self.dev(a["blocks"]), a["max_prefix"], self.d ** -0.5,
+            self.dev(a["start"]), self.dev(a["blocks"]), a["max_prefix"], self.scale,
             max_suffix_len=a["max_suffix_len"], k_scale=self.ks, v_scale=self.vs, workspace=a["workspace"],
             stream=a["stream"])
 
@@ -108,14 +109,14 @@ class Batch:
         to = to_u8 if self.fp8 else to_u16
         return oracle.paged_decode(to_u16(self.q), to(self.k if k is None else k), to(self.v if v is None else v),
                                    self.tables if tables is None else tables,
-                                   (self.lens if lens is None else lens).astype(np.int32), self.d ** -0.5,
+                                   (self.lens if lens is None else lens).astype(np.int32), self.scale,
                                    kv_dtype=oracle.KV_FP8_E4M3 if self.fp8 else oracle.KV_BF16, k_scale=self.ks,
                                    v_scale=self.vs, seq_subset=subset)
 
     def tol(self):
         # Z: sm_scale sum |q k| <= sm_scale |q| |k| (Cauchy-Schwarz on the largest rows)
         kk = self.k.float().nan_to_num(0.0) * self.ks
-        Z = self.d ** -0.5 * float(self.q.float().norm(dim=-1).max()) * float(kk.norm(dim=-1).max())
+        Z = abs(self.scale) * float(self.q.float().norm(dim=-1).max()) * float(kk.norm(dim=-1).max())
         n = max(int(self.lens.max()), 1)
         return 2 * self.vmax * (10 * 2.0 ** -23 * Z + 2.0 ** -21 * (1 + Z / 8) + 2.0 ** -17
                                 + (n / 128 + 16) * 2.0 ** -23)
@@ -164,6 +165,17 @@ def test_matches_the_oracle(hq, hkv, d, sizes, prefixes, lo, hi, fp8):
 @pytest.mark.parametrize("spread", [6.0, 24.0])
 def test_peaked_scores(spread, fp8):
     b = Batch(8, 2, 128, [11], [40], suffixes(3, 11, 0, 300), fp8=fp8, seed=2, spread=spread)
+    b.check(b.run())
+    assert pa_get_device_error() == 0
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("scale", [-0.11, 0.0, 1e-3])
+def test_any_finite_scale(scale, fp8):
+    """A negative scale turns the order of the scores around, zero makes all
+    weights equal; a prefix that ends inside a key tile is masked either way."""
+    b = Batch(8, 2, 128, [7], [13], suffixes(9, 7, 0, 90), fp8=fp8, seed=21)
+    b.scale = scale
     b.check(b.run())
     assert pa_get_device_error() == 0
 

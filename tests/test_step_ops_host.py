@@ -131,6 +131,7 @@ def test_rope_rejects_bad_arguments_on_host(kw, expect):
 @pytest.mark.parametrize("kw,expect", [
     (dict(B=8), UNSUPPORTED),
     (dict(S=16385), UNSUPPORTED),
+    (dict(W=1 << 27), UNSUPPORTED),
     (dict(S=-1), INVALID),
     (dict(T=-1), INVALID),
     (dict(W=-1), INVALID),
@@ -157,6 +158,7 @@ def test_extend_rejects_bad_arguments_on_host(kw, expect):
 @pytest.mark.parametrize("kw,expect", [
     (dict(B=8), UNSUPPORTED),
     (dict(S=16385), UNSUPPORTED),
+    (dict(W=1 << 27), UNSUPPORTED),
     (dict(keep=-1), INVALID),
     (dict(S=-1), INVALID),
     (dict(rel=None), INVALID),
@@ -176,6 +178,7 @@ def test_release_rejects_bad_arguments_on_host(kw, expect):
     (dict(S=-1), INVALID),
     (dict(G=-1), INVALID),
     (dict(G=65536), UNSUPPORTED),
+    (dict(maxb=1 << 27), UNSUPPORTED),
     (dict(maxp=-1), INVALID),
     (dict(maxs=-1), INVALID),
     (dict(B=8), UNSUPPORTED),
