@@ -23,8 +23,8 @@ import torch
 
 import synth
 
-from . import (BlockPool, pa_copy_blocks, pa_decode, pa_decode_append, pa_decode_workspace_size,
-               pa_reshape_and_cache)
+from . import (BlockPool, pa_copy_blocks, pa_decode, pa_decode_append, pa_decode_shared_prefix,
+               pa_decode_workspace_size, pa_reshape_and_cache)
 
 BS = 16
 
@@ -198,6 +198,25 @@ class DecodeBatch:
         """One decode step: write the new tokens (after any CoW copy), decode."""
         self.run_ops(self.step_ops, stream=stream)
         return self.decode(partition_size=partition_size, workspace=workspace, stream=stream)
+
+    def step_shared(self, workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """The same step with the batch decoded as one group behind its shared
+        prefix (pa_decode_shared_prefix): the prefix's full blocks are read
+        and multiplied once for all sequences. A batch without a prefix is a
+        group whose sequences share nothing."""
+        if not hasattr(self, "_group_start"):
+            blocks = self.w.prefix_len // BS
+            self._group_start = torch.tensor([0, self.w.num_seqs], dtype=torch.int32, device=self.device)
+            self._prefix_blocks = torch.tensor([blocks], dtype=torch.int32, device=self.device)
+        blocks = self.w.prefix_len // BS
+        self.run_ops(self.step_ops, stream=stream)
+        return pa_decode_shared_prefix(self.out, self.q, self.k_cache, self.v_cache,
+                                       self.block_tables, self.context_lens, self.max_context_len,
+                                       self._group_start, self._prefix_blocks, blocks,
+                                       self.w.sm_scale,
+                                       max_suffix_len=self.max_context_len - blocks * BS,
+                                       k_scale=self.k_scale, v_scale=self.v_scale,
+                                       workspace=workspace, stream=stream)
 
     def step_fused(self, partition_size: Optional[int] = None,
                    workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
