@@ -14,15 +14,28 @@
 // stack first), and its token t (Q_s <= t < Q_s + n_s) stands at position
 // p = L_s + t - Q_s in slot table[s][p / 16] * 16 + p % 16.
 //
-// What bounds it: latency for a decode step (a few KB), the slots' and
-// positions' 12 bytes a token for large admissions. The two exclusive sums
-// over the rows are the only dependence: every CTA scans all the rows itself
-// (two integers a row, from L2) into shared memory, where the row of a token
-// or a block is then found by bisection, so no partial sums travel between
-// CTAs. The lengths and the count may be updated in place, so they are
-// written only when no CTA reads them any more: a small call is one CTA with
-// a barrier between, a large one a launch over the GPU for the tokens and a
-// one-CTA launch for the lengths and the count (TablePhase).
+// What bounds it. A decode step moves a few KB: the chain launch, lengths,
+// sums, ids, stores (3.1 us for 128 rows of one token, in a graph). A large
+// admission writes 12 bytes a token (4.7 us at the copy rate for 2.6 million
+// tokens of 2000 rows), but spends its time on issuing instructions, about
+// 100 a token: 16 us, of which the sums take 4. The two exclusive sums over the rows are
+// the only dependence: every CTA scans all the rows itself (two integers a
+// row, from L2) into shared memory, where the row of a token or a block is
+// then found by bisection, so no partial sums travel between CTAs. A thread
+// takes four neighbours, which mostly are of one row: one search, one or two
+// ids (all read before an entry is stored, since a store between them would
+// hold the next read back), whole sectors out.
+//
+// The lengths and the count may be updated in place, so they are written
+// only when no CTA reads them any more (TablePhase): a small call is one CTA
+// with a barrier between, a large one a launch over the GPU for the tokens
+// and a one-CTA launch that sums the rows beside it on an SM left free and
+// writes the lengths and the count when it has ended. One CTA against two
+// launches, in a graph, 128 rows: extend 3.5 us against 3.7 at 2048 tokens,
+// 4.4 against 3.9 at 4096; release at a bound of 8192 blocks 3.7 against 3.9
+// with few rows ended and 6.6 against 3.9 with all of them, at 16384 3.9 and
+// 9.9 against 4.0. The second launch costs the host 2 us, so one CTA is kept
+// to 2048 tokens and 8192 blocks.
 #pragma once
 
 #include "decode.cuh"
@@ -33,9 +46,8 @@ namespace pa {
 constexpr int kTabThreads = 1024;
 constexpr int kTabMaxSeqs = 16384;        // rows whose sums one CTA's shared memory holds
 constexpr int kTabBatch = 4;              // tokens or blocks of a thread in flight
-constexpr int kTabPerCta = kTabThreads * kTabBatch;   // of a CTA of kTabThreads
-constexpr int kTabSmallTokens = 2 * kTabPerCta;   // extend: one CTA up to here
-constexpr int kTabSmallBlocks = 8 * kTabPerCta;   // release: one CTA up to this bound of its pushes
+constexpr int kTabSmallTokens = 2048;     // extend: one CTA up to here
+constexpr int kTabSmallBlocks = 8192;    // release: one CTA up to this bound of its pushes
 
 constexpr uint32_t kErrOutOfBlocks = 0x20u;
 constexpr uint32_t kErrLengthRange = 0x40u;
@@ -122,6 +134,7 @@ struct ExtendParams {
 template <TablePhase PHASE>
 __global__ void __launch_bounds__(kTabThreads) extend_kernel(const ExtendParams p) {
   extern __shared__ int32_t s_rows[];
+  if (PHASE == TablePhase::kWork) launch_dependents();
   const int S = p.num_seqs;
   int32_t *s_query = s_rows;           // [S + 1] tokens of earlier rows
   int32_t *s_first = s_query + S + 1;  // [S] blocks needed by earlier rows
@@ -130,12 +143,13 @@ __global__ void __launch_bounds__(kTabThreads) extend_kernel(const ExtendParams 
   const int s0 = min(S, static_cast<int>(threadIdx.x) * per), s1 = min(S, s0 + per);
   const int64_t row_cap = static_cast<int64_t>(p.max_blocks_per_seq) * kBS;
   const int count = *p.free_count;
-  auto need = [](int64_t L, int64_t n) { return (L + n + kBS - 1) / kBS - (L + kBS - 1) / kBS; };
+  // (of lengths out of range, whose sums are not used, anything)
+  auto need = [](uint32_t L, uint32_t n) { return (L + n + kBS - 1) / kBS - (L + kBS - 1) / kBS; };
   Two mine{0, 0};
   bool bad = false;
   for (int s = s0; s < s1; ++s) {
-    const int64_t L = p.context_lens[s], n = p.new_lens[s];
-    bad |= L < 0 || n < 0 || L + n > row_cap;
+    const int L = p.context_lens[s], n = p.new_lens[s];
+    bad |= L < 0 || n < 0 || static_cast<int64_t>(L) + n > row_cap;
     mine.a += n;
     mine.b += need(L, n);
   }
@@ -155,10 +169,10 @@ __global__ void __launch_bounds__(kTabThreads) extend_kernel(const ExtendParams 
     const int tokens = ok ? static_cast<int>(total.a) : 0;
     int64_t q = first.a, b = first.b;
     for (int s = s0; s < s1; ++s) {
-      const int64_t L = p.context_lens[s], n = p.new_lens[s];
+      const int L = p.context_lens[s], n = p.new_lens[s];
       s_query[s] = ok ? static_cast<int>(q) : 0;
       s_first[s] = static_cast<int>(b);
-      s_len[s] = static_cast<int>(L);
+      s_len[s] = L;
       if (blockIdx.x == 0) p.query_start[s] = ok ? static_cast<int>(q) : 0;
       q += n;
       b += need(L, n);
@@ -169,78 +183,89 @@ __global__ void __launch_bounds__(kTabThreads) extend_kernel(const ExtendParams 
     }
     __syncthreads();
     bool bad_id = false;
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x * kTabBatch;
-    for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) * kTabBatch;
-         t0 < p.num_tokens; t0 += stride) {
+    const uint32_t total_tokens = p.num_tokens, stride = gridDim.x * blockDim.x * kTabBatch;
+    // where the id of block j of row s is read: its table or, behind the
+    // row's `old` blocks, the stack
+    auto source = [&](int s, uint32_t j, uint32_t old) -> const int32_t * {
+      return j < old ? p.block_tables + static_cast<int64_t>(s) * p.max_blocks_per_seq + j
+                     : p.free_blocks + (count - 1 - s_first[s] - static_cast<int>(j - old));
+    };
+    auto put_entry = [&](int s, uint32_t j, int id) {
+      p.block_tables[static_cast<int64_t>(s) * p.max_blocks_per_seq + j] = id;
+    };
+    // slot of position x in block id, as two words
+    auto put_slot = [&](uint32_t *w, int id, uint32_t x) {
+      const bool in_pool = static_cast<uint32_t>(id) < static_cast<uint32_t>(p.num_blocks);
+      const uint64_t slot = in_pool ? static_cast<uint64_t>(id) * kBS + x % kBS : ~0ull;
+      w[0] = static_cast<uint32_t>(slot);
+      w[1] = static_cast<uint32_t>(slot >> 32);
+      bad_id |= !in_pool;
+    };
+    for (uint32_t t0 = (blockIdx.x * blockDim.x + threadIdx.x) * kTabBatch; t0 < total_tokens; t0 += stride) {
       // four consecutive tokens: their rows, then their block ids, then the stores
-      int pos[kTabBatch], id[kTabBatch];
+      uint32_t pos[kTabBatch] = {}, w[2 * kTabBatch];
 #pragma unroll
-      for (int i = 0; i < kTabBatch; ++i) {
-        pos[i] = 0;
-        id[i] = -1;
-      }
-      const int live = static_cast<int>(min(static_cast<int64_t>(kTabBatch), tokens - t0));  // <= 0: padding
-      // the id of block j of row s, from its table or the stack; a new
-      // block's entry is written by the thread of its first token
-      auto block_id = [&](int s, int j, int old, bool starts) {
-        int32_t *entry = p.block_tables + static_cast<int64_t>(s) * p.max_blocks_per_seq + j;
-        if (j < old) return *entry;
-        const int b = p.free_blocks[count - 1 - (s_first[s] + j - old)];
-        if (starts) *entry = b;
-        return b;
-      };
+      for (int i = 0; i < 2 * kTabBatch; ++i) w[i] = 0xffffffffu;
+      const int live = min(kTabBatch, tokens - static_cast<int>(t0));  // <= 0: padding
       if (live > 0) {
         const int v[1] = {static_cast<int>(t0)};
         int k[1] = {-1};
         // rows of few tokens are looked up one token at a time
-        if (p.num_tokens > kTabBatch * S) last_not_above(s_query, S, v, k);
+        if (total_tokens > static_cast<uint32_t>(kTabBatch) * S) last_not_above(s_query, S, v, k);
         if (k[0] >= 0 && v[0] + live <= s_query[k[0] + 1]) {  // one row: its positions follow one another, in two blocks at most
-          const int s = k[0], L = s_len[s], old = (L + kBS - 1) / kBS;
-          const int p0 = L + v[0] - s_query[s], off = p0 % kBS, next = (p0 + live - 1) / kBS;
-          const int id0 = block_id(s, p0 / kBS, old, off == 0);
-          const int id1 = next != p0 / kBS ? block_id(s, next, old, true) : id0;
+          const int s = k[0];
+          const uint32_t L = s_len[s], old = (L + kBS - 1) / kBS, p0 = L + (t0 - s_query[s]), last = p0 + live - 1;
+          const uint32_t j0 = p0 / kBS, j1 = last / kBS;
+          // both ids are on their way before an entry is stored
+          const int id0 = *source(s, j0, old);
+          const int id1 = j1 != j0 ? *source(s, j1, old) : id0;
+          // a new block's entry is written by the thread of its first token
+          if (p0 % kBS == 0 && j0 >= old) put_entry(s, j0, id0);
+          if (j1 != j0 && j1 >= old) put_entry(s, j1, id1);
 #pragma unroll
           for (int i = 0; i < kTabBatch; ++i)
             if (i < live) {
               pos[i] = p0 + i;
-              id[i] = off + i < kBS ? id0 : id1;
+              put_slot(w + 2 * i, pos[i] / kBS == j0 ? id0 : id1, pos[i]);
             }
         } else {
-          int t[kTabBatch], s[kTabBatch];
+          int t[kTabBatch], s[kTabBatch], id[kTabBatch];
+          uint32_t old[kTabBatch];
 #pragma unroll
           for (int i = 0; i < kTabBatch; ++i) t[i] = v[0] + min(i, live - 1);
-          last_not_above(s_query, S, t, s);
+          if (k[0] >= 0 && v[0] + live <= s_query[min(k[0] + 2, S)]) {  // this row and the next
+#pragma unroll
+            for (int i = 0; i < kTabBatch; ++i) s[i] = k[0] + (t[i] >= s_query[k[0] + 1]);
+          } else {
+            last_not_above(s_query, S, t, s);
+          }
+#pragma unroll
+          for (int i = 0; i < kTabBatch; ++i) {
+            const uint32_t L = s_len[s[i]];
+            old[i] = (L + kBS - 1) / kBS;
+            pos[i] = L + (t[i] - s_query[s[i]]);
+            id[i] = *source(s[i], pos[i] / kBS, old[i]);
+          }
 #pragma unroll
           for (int i = 0; i < kTabBatch; ++i)
             if (i < live) {
-              const int L = s_len[s[i]];
-              pos[i] = L + t[i] - s_query[s[i]];
-              id[i] = block_id(s[i], pos[i] / kBS, (L + kBS - 1) / kBS, pos[i] % kBS == 0);
+              const uint32_t j = pos[i] / kBS;
+              if (pos[i] % kBS == 0 && j >= old[i]) put_entry(s[i], j, id[i]);
+              put_slot(w + 2 * i, id[i], pos[i]);
+            } else {
+              pos[i] = 0;
             }
         }
       }
-      int64_t slot[kTabBatch];
-#pragma unroll
-      for (int i = 0; i < kTabBatch; ++i) {
-        const bool in_pool = id[i] >= 0 && id[i] < p.num_blocks;
-        bad_id |= i < live && !in_pool;
-        slot[i] = in_pool ? static_cast<int64_t>(id[i]) * kBS + pos[i] % kBS : -1;
-      }
-      if (p.wide && t0 + kTabBatch <= p.num_tokens) {  // whole sectors
-        uint32_t w[2 * kTabBatch];
-#pragma unroll
-        for (int i = 0; i < kTabBatch; ++i) {
-          w[2 * i] = static_cast<uint32_t>(slot[i]);
-          w[2 * i + 1] = static_cast<uint32_t>(slot[i] >> 32);
-        }
+      if (p.wide && t0 + kTabBatch <= total_tokens) {  // whole sectors
         st_global_v8(p.slot_mapping + t0, w);
-        *reinterpret_cast<int4 *>(p.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+        *reinterpret_cast<uint4 *>(p.positions + t0) = make_uint4(pos[0], pos[1], pos[2], pos[3]);
       } else {
 #pragma unroll
         for (int i = 0; i < kTabBatch; ++i)
-          if (t0 + i < p.num_tokens) {
-            p.slot_mapping[t0 + i] = slot[i];
-            p.positions[t0 + i] = pos[i];
+          if (t0 + i < total_tokens) {
+            p.slot_mapping[t0 + i] = static_cast<int64_t>(static_cast<uint64_t>(w[2 * i + 1]) << 32 | w[2 * i]);
+            p.positions[t0 + i] = static_cast<int>(pos[i]);
           }
       }
     }
@@ -281,6 +306,7 @@ __device__ __forceinline__ int64_t released_blocks(const ReleaseParams &p, int s
 template <TablePhase PHASE>
 __global__ void __launch_bounds__(kTabThreads) release_kernel(const ReleaseParams p) {
   extern __shared__ int32_t s_first[];  // [S] blocks pushed by earlier rows
+  if (PHASE == TablePhase::kWork) launch_dependents();
   const int S = p.num_seqs;
   const int per = (S + blockDim.x - 1) / blockDim.x;
   const int s0 = min(S, static_cast<int>(threadIdx.x) * per), s1 = min(S, s0 + per);
@@ -306,21 +332,30 @@ __global__ void __launch_bounds__(kTabThreads) release_kernel(const ReleaseParam
       b += released_blocks(p, s);
     }
     __syncthreads();
-    const int stride = gridDim.x * blockDim.x;
+    const uint32_t stride = gridDim.x * blockDim.x * kTabBatch;
     bool bad_id = false;
-    for (int64_t k0 = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; k0 < blocks; k0 += kTabBatch * stride) {
-      int k[kTabBatch], s[kTabBatch], id[kTabBatch];
+    for (uint32_t k0 = (blockIdx.x * blockDim.x + threadIdx.x) * kTabBatch; k0 < static_cast<uint32_t>(blocks); k0 += stride) {
+      // four consecutive pushes, mostly of one row or of two neighbours
+      const int k = k0, more = min(kTabBatch, blocks - k) - 1;
+      const int first_k[1] = {k};
+      int r[1];
+      last_not_above(s_first, S, first_k, r);
+      const int next = r[0] + 1 < S ? s_first[r[0] + 1] : blocks, after = r[0] + 2 < S ? s_first[r[0] + 2] : blocks;
+      int s[kTabBatch], id[kTabBatch], kk[kTabBatch];
 #pragma unroll
-      for (int i = 0; i < kTabBatch; ++i) k[i] = static_cast<int>(min(k0 + i * stride, static_cast<int64_t>(blocks - 1)));
-      last_not_above(s_first, S, k, s);
+      for (int i = 0; i < kTabBatch; ++i) {
+        kk[i] = k + min(i, more);
+        s[i] = r[0] + (kk[i] >= next);
+      }
+      if (k + more >= after) last_not_above(s_first, S, kk, s);
 #pragma unroll
       for (int i = 0; i < kTabBatch; ++i)
-        id[i] = p.block_tables[static_cast<int64_t>(s[i]) * p.max_blocks_per_seq + p.keep_blocks + k[i] - s_first[s[i]]];
+        id[i] = p.block_tables[static_cast<int64_t>(s[i]) * p.max_blocks_per_seq + p.keep_blocks + kk[i] - s_first[s[i]]];
 #pragma unroll
       for (int i = 0; i < kTabBatch; ++i)
-        if (k0 + i * stride < blocks) {
+        if (i <= more) {
           bad_id |= id[i] < 0 || id[i] >= p.num_blocks;
-          p.free_blocks[count + k[i]] = id[i];
+          p.free_blocks[count + kk[i]] = id[i];
         }
     }
     if (bad_id) raise_error(kErrBlockRange);

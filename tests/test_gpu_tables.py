@@ -347,3 +347,84 @@ def test_steps_in_a_graph_follow_the_host_pool():
     assert pa_get_device_error() == 0
     del graph
     assert torch.count_nonzero(rel0) == 0
+
+
+def uneven(g, S, long):
+    """Rows of 0, 1, 2, 3 and many tokens beside one another, in runs."""
+    kinds = g.choice(6, S, p=[0.3, 0.2, 0.15, 0.1, 0.1, 0.15])
+    return np.where(kinds < 4, kinds, g.integers(4, long, S))
+
+
+@pytest.mark.parametrize("S,long,pad,offset", [
+    (64, 40, 0, 0),        # one CTA
+    (90, 130, 3, 1),       # about 2048 tokens, outputs off their alignment
+    (700, 200, 17, 0),     # a large call whose threads meet up to four rows
+    (3000, 90, 1, 3),
+])
+def test_extend_rows_of_uneven_lengths(S, long, pad, offset):
+    g, tables, lens, free, count, nb = state(S + long, S, 24, 150, nb_spare=S * 16)
+    new = uneven(g, S, long)
+    new = np.minimum(new, 24 * B - lens)
+    T = int(new.sum()) + pad
+    got = run_extend(tables, lens, new, free, count, T, nb, offset=offset)
+    check_extend(got, plain_extend(tables, lens, new, free, count, T, nb))
+
+
+@pytest.mark.parametrize("tokens", [2047, 2048, 2049, 4096, 4097])
+def test_extend_where_the_calls_split(tokens):
+    """The two sides of the one-CTA rule give the same."""
+    g, tables, lens, free, count, nb = state(tokens, 5, 200, 600, nb_spare=400)
+    new = np.full(5, tokens // 5)
+    new[2] += tokens - int(new.sum())
+    got = run_extend(tables, lens, new, free, count, tokens, nb)
+    check_extend(got, plain_extend(tables, lens, new, free, count, tokens, nb))
+
+
+@pytest.mark.parametrize("keep", [0, 2])
+@pytest.mark.parametrize("S,W", [(64, 128), (64, 130), (700, 24), (3000, 9)])
+def test_release_rows_of_uneven_lengths(S, W, keep):
+    g = np.random.default_rng(S + W + keep)
+    blocks = np.minimum(uneven(g, S, W + 1), W)
+    lens = np.maximum(blocks * B - g.integers(0, B, S), 0)
+    held = -(-lens // B)
+    nb = int(held.sum()) + 3
+    tables = np.full((S, W), -1, np.int32)
+    ids = g.permutation(nb)
+    for s, e in enumerate(np.cumsum(held)):
+        tables[s, :held[s]] = ids[e - held[s]:e]
+    rel = (g.random(S) < 0.8).astype(np.int32)
+    free = np.full(nb + 5, -7, np.int32)
+    fr, ct, ln = dev(free), dev([2]), dev(lens)
+    pa_release_tables(dev(tables), ln, dev(rel), fr, ct, ln, ct, keep_blocks=keep, num_blocks=nb)
+    want, wl, wc, flags = plain_release(tables, lens, rel, free, 2, keep, nb)
+    np.testing.assert_array_equal(fr.cpu().numpy(), want)
+    np.testing.assert_array_equal(ln.cpu().numpy(), wl)
+    assert int(ct) == wc and pa_get_device_error() == flags == 0
+
+
+def test_calls_behind_one_another_see_each_others_results():
+    """Large calls in place, without a synchronisation between: the next
+    call's first launch must find the last one's lengths and count."""
+    g, tables, lens, free, count, nb = state(5, 600, 40, 60, nb_spare=30000)
+    t, ln, fr, ct = dev(tables), dev(lens), dev(free), dev([count])
+    news = [g.integers(0, 30, 600) for _ in range(8)]
+    rels = [(g.random(600) < 0.3).astype(np.int32) for _ in range(8)]
+    T = 20000
+    sl = torch.empty(T, dtype=torch.int64, device="cuda")
+    ps, qs = torch.empty(T, dtype=torch.int32, device="cuda"), torch.empty(601, dtype=torch.int32, device="cuda")
+    dn, dr = [dev(n) for n in news], [dev(r) for r in rels]
+    torch.cuda.synchronize()
+    for n, r in zip(dn, dr):
+        pa_extend_tables(t, ln, n, fr, ct, ln, ct, sl, ps, qs, num_blocks=nb)
+        pa_release_tables(t, ln, r, fr, ct, ln, ct, num_blocks=nb)
+    for n, r in zip(news, rels):
+        tables, lens, count, slots, pos, start, flags = plain_extend(tables, lens, n, free, count, T, nb)
+        assert flags == 0
+        free, lens, count, flags = plain_release(tables, lens, r, free, count, 0, nb)
+        assert flags == 0
+    np.testing.assert_array_equal(t.cpu().numpy(), tables)
+    np.testing.assert_array_equal(ln.cpu().numpy(), lens)
+    np.testing.assert_array_equal(fr.cpu().numpy()[:count], free[:count])
+    np.testing.assert_array_equal(sl.cpu().numpy(), slots)
+    np.testing.assert_array_equal(ps.cpu().numpy(), pos)
+    assert int(ct) == count and pa_get_device_error() == 0
