@@ -236,7 +236,7 @@ SharedPlan shared_plan(int num_seqs, int num_q_heads, int num_kv_heads, int head
                     : 0;
   // Prefix parts, of at most kSpPartTiles key tiles: the number that makes
   // waves x (key tiles of a part + 2) smallest; two tiles stand for a CTA's
-  // start and its output.
+  // start and its output (four in their place chose the same parts).
   if (s.row_tiles > 0) {
     const int64_t tiles = (max_prefix_blocks + pa::kSpBlocks - 1) / pa::kSpBlocks;
     const int64_t units = static_cast<int64_t>(s.row_tiles) * num_kv_heads;
@@ -251,10 +251,13 @@ SharedPlan shared_plan(int num_seqs, int num_q_heads, int num_kv_heads, int head
       }
     }
   }
-  // Suffix parts: about four waves of resident CTAs (3 per SM), at least 256
-  // tokens each.
+  // Suffix parts: about three waves of resident CTAs (3 per SM), at least 256
+  // tokens each. Suffixes alone, bf16, 32 query and 8 KV heads: 16 sequences
+  // of up to 4096 tokens 33.3 us (two waves 34.8, four 35.8), 64 of up to
+  // 1024 33.3 (37.0, 35.8), 4 of up to 8192 16.0 (15.5, 16.0); 4 of up to
+  // 1000 with 32 KV heads 11.6 (13.5 with parts of 128 tokens, 15.5 of 512).
   const int64_t units = std::max<int64_t>(static_cast<int64_t>(num_seqs) * num_kv_heads, 1);
-  const int64_t wanted = std::max<int64_t>(1, 4 * 3 * kSms / units);
+  const int64_t wanted = std::max<int64_t>(1, 3 * 3 * kSms / units);
   int64_t len = (max_suffix_len + wanted - 1) / wanted;
   len = std::max<int64_t>((len + 127) / 128 * 128, 256);
   s.part_len = static_cast<int>(std::min<int64_t>(len, INT32_MAX / 128 * 128));

