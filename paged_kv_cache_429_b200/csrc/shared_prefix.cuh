@@ -1144,7 +1144,10 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 3 : 2)
 
 // One warp a row (sequence, query head), its prefix records and its own parts:
 //     out = out_scale sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i,
-// kJoinBatch records in flight, M the maximum so far.
+// kJoinBatch records in flight, M the maximum so far. Bound by L2: the long
+// prefix's 19 records a row are 41 MB. Whole calls with two, four and eight
+// in flight: 10.0, 9.4, 9.6 us (4 sequences), 152, 150, 150 (64 sequences
+// behind 32768 tokens).
 constexpr int kJoinBatch = 4;
 
 template <int D>
