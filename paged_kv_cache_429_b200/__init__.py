@@ -148,6 +148,14 @@ def _status(rc, what: str) -> bool:
     return rc is not None
 
 
+def _int32(v, name: str) -> int:
+    """A size as the library takes it (ctypes would drop the upper bits)."""
+    v = int(v)
+    if not -2**31 <= v < 2**31:
+        raise OverflowError(f"{name}: {v} does not fit 32 bits")
+    return v
+
+
 def _raw_stream(stream: Optional[torch.cuda.Stream], dev: int) -> int:
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
@@ -325,8 +333,9 @@ def pa_decode_shared_prefix(out: torch.Tensor, q: torch.Tensor, k_cache: torch.T
         raise ValueError("block_tables / context_lens must have num_seqs rows")
     if group_start.shape[0] != G + 1:
         raise ValueError("group_start must have one entry more than prefix_blocks")
-    max_context_len, max_prefix_blocks = int(max_context_len), int(max_prefix_blocks)
-    suffix = max_context_len if max_suffix_len is None else int(max_suffix_len)
+    max_context_len = _int32(max_context_len, "max_context_len")
+    max_prefix_blocks = _int32(max_prefix_blocks, "max_prefix_blocks")
+    suffix = max_context_len if max_suffix_len is None else _int32(max_suffix_len, "max_suffix_len")
     st = _raw_stream(stream, dev)
     if workspace is None:
         # allocated for the stream that uses it
@@ -340,9 +349,9 @@ def pa_decode_shared_prefix(out: torch.Tensor, q: torch.Tensor, k_cache: torch.T
         raise ValueError("the workspace must be on the device of the call's tensors")
     _call("pa_decode_shared_prefix", dev,
           out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-          kv_dtype_of(k_cache), k_scale, v_scale, block_tables.data_ptr(), block_tables.shape[1],
+          kv_dtype_of(k_cache), float(k_scale), float(v_scale), block_tables.data_ptr(), block_tables.shape[1],
           context_lens.data_ptr(), max_context_len, group_start.data_ptr(), prefix_blocks.data_ptr(),
-          G, max_prefix_blocks, suffix, S, Hq, Hkv, D, B, NB, sm_scale, workspace.data_ptr(),
+          G, max_prefix_blocks, suffix, S, Hq, Hkv, D, B, NB, float(sm_scale), workspace.data_ptr(),
           workspace.numel() * workspace.element_size(), st)
     return out
 
@@ -481,9 +490,9 @@ def pa_rope_and_cache(q_out: torch.Tensor, q: torch.Tensor, key: torch.Tensor,
     _call("pa_rope_and_cache", dev,
           q_out.data_ptr(), q.data_ptr(), key.data_ptr(), value.data_ptr(), k_cache.data_ptr(),
           v_cache.data_ptr(), slot_mapping.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(),
-          2 * inv_freq.shape[0], 1 if interleaved else 0, rope_scale, _row_stride(q),
+          2 * inv_freq.shape[0], 1 if interleaved else 0, float(rope_scale), _row_stride(q),
           _row_stride(key), _row_stride(value), T, Hq, Hkv, D, B, NB, kv_dtype_of(k_cache),
-          k_scale, v_scale, _raw_stream(stream, dev))
+          float(k_scale), float(v_scale), _raw_stream(stream, dev))
     return q_out
 
 
@@ -506,7 +515,7 @@ def pa_extend_tables(block_tables: torch.Tensor, context_lens: torch.Tensor,
             (_lib._ext or _lib.binding()).extend_tables(
                 block_tables, context_lens, new_lens, free_blocks, free_count, context_lens_out,
                 free_count_out, slot_mapping, positions, query_start,
-                -1 if num_blocks is None else num_blocks), "pa_extend_tables"):
+                num_blocks), "pa_extend_tables"):
         return
     dev = _check_all((block_tables, context_lens, new_lens, free_blocks, free_count,
                       context_lens_out, free_count_out, slot_mapping, positions, query_start),
@@ -524,7 +533,7 @@ def pa_extend_tables(block_tables: torch.Tensor, context_lens: torch.Tensor,
           block_tables.data_ptr(), W, context_lens.data_ptr(), new_lens.data_ptr(),
           free_blocks.data_ptr(), capacity, free_count.data_ptr(), context_lens_out.data_ptr(),
           free_count_out.data_ptr(), slot_mapping.data_ptr(), positions.data_ptr(),
-          query_start.data_ptr(), S, T, BLOCK_SIZE, capacity if num_blocks is None else int(num_blocks),
+          query_start.data_ptr(), S, T, BLOCK_SIZE, capacity if num_blocks is None else _int32(num_blocks, "num_blocks"),
           _raw_stream(stream, dev))
 
 
@@ -546,7 +555,7 @@ def pa_release_tables(block_tables: torch.Tensor, context_lens: torch.Tensor,
     if stream is None and _status(
             (_lib._ext or _lib.binding()).release_tables(
                 block_tables, context_lens, release, free_blocks, free_count, context_lens_out,
-                free_count_out, keep_blocks, -1 if num_blocks is None else num_blocks),
+                free_count_out, keep_blocks, num_blocks),
             "pa_release_tables"):
         return
     dev = _check_all((block_tables, context_lens, release, free_blocks, free_count,
@@ -560,8 +569,8 @@ def pa_release_tables(block_tables: torch.Tensor, context_lens: torch.Tensor,
     _call("pa_release_tables", dev,
           block_tables.data_ptr(), W, context_lens.data_ptr(), release.data_ptr(),
           free_blocks.data_ptr(), capacity, free_count.data_ptr(), context_lens_out.data_ptr(),
-          free_count_out.data_ptr(), int(keep_blocks), S, BLOCK_SIZE,
-          capacity if num_blocks is None else int(num_blocks), _raw_stream(stream, dev))
+          free_count_out.data_ptr(), _int32(keep_blocks, "keep_blocks"), S, BLOCK_SIZE,
+          capacity if num_blocks is None else _int32(num_blocks, "num_blocks"), _raw_stream(stream, dev))
 
 
 _RELEASE_SPECS = (("block_tables", _I32, 2), ("context_lens", _I32, 1), ("release", _I32, 1),

@@ -117,7 +117,7 @@ bool small(const at::Tensor *t) { return t->numel() <= INT32_MAX; }
 
 // (block_tables, context_lens, new_lens, free_blocks, free_count,
 // context_lens_out, free_count_out, slot_mapping, positions, query_start,
-// num_blocks or -1)
+// num_blocks or None)
 PyObject *extend_tables(PyObject *const *args, Py_ssize_t n) {
   if (n != 11) Py_RETURN_NONE;
   Call c{args};
@@ -125,13 +125,14 @@ PyObject *extend_tables(PyObject *const *args, Py_ssize_t n) {
                    *free = c.typed(3, 1, at::kInt), *count = c.typed(4, 1, at::kInt),
                    *lens_out = c.typed(5, 1, at::kInt), *count_out = c.typed(6, 1, at::kInt),
                    *slots = c.typed(7, 1, at::kLong), *pos = c.typed(8, 1, at::kInt), *qs = c.typed(9, 1, at::kInt);
-  int nb = c.integer(10);
+  const bool whole = args[10] == Py_None;  // the pool is as large as the stack
+  int nb = whole ? 0 : c.integer(10);
   if (!c.ready() || !small(slots) || !small(free)) Py_RETURN_NONE;
   const int64_t S = bt->size(0);
   if (lens->size(0) != S || more->size(0) != S || lens_out->size(0) != S || count->size(0) != 1 ||
       count_out->size(0) != 1 || pos->size(0) != slots->size(0) || qs->size(0) != S + 1)
     Py_RETURN_NONE;
-  if (nb < 0) nb = len(free, 0);
+  if (whole) nb = len(free, 0);
   return status_of([&] {
     return pa_extend_tables(ptr<int32_t>(bt), len(bt, 1), ptr<int32_t>(lens), ptr<int32_t>(more), ptr<int32_t>(free),
                             len(free, 0), ptr<int32_t>(count), ptr<int32_t>(lens_out), ptr<int32_t>(count_out),
@@ -141,7 +142,7 @@ PyObject *extend_tables(PyObject *const *args, Py_ssize_t n) {
 }
 
 // (block_tables, context_lens, release, free_blocks, free_count,
-// context_lens_out, free_count_out, keep_blocks, num_blocks or -1)
+// context_lens_out, free_count_out, keep_blocks, num_blocks or None)
 PyObject *release_tables(PyObject *const *args, Py_ssize_t n) {
   if (n != 9) Py_RETURN_NONE;
   Call c{args};
@@ -149,13 +150,14 @@ PyObject *release_tables(PyObject *const *args, Py_ssize_t n) {
                    *free = c.typed(3, 1, at::kInt), *count = c.typed(4, 1, at::kInt),
                    *lens_out = c.typed(5, 1, at::kInt), *count_out = c.typed(6, 1, at::kInt);
   const int keep = c.integer(7);
-  int nb = c.integer(8);
+  const bool whole = args[8] == Py_None;
+  int nb = whole ? 0 : c.integer(8);
   if (!c.ready() || !small(free)) Py_RETURN_NONE;
   const int64_t S = bt->size(0);
   if (lens->size(0) != S || rel->size(0) != S || lens_out->size(0) != S || count->size(0) != 1 ||
       count_out->size(0) != 1)
     Py_RETURN_NONE;
-  if (nb < 0) nb = len(free, 0);
+  if (whole) nb = len(free, 0);
   return status_of([&] {
     return pa_release_tables(ptr<int32_t>(bt), len(bt, 1), ptr<int32_t>(lens), ptr<int32_t>(rel), ptr<int32_t>(free),
                              len(free, 0), ptr<int32_t>(count), ptr<int32_t>(lens_out), ptr<int32_t>(count_out), keep,

@@ -266,3 +266,35 @@ def test_the_binding_says_what_is_wrong():
         pa.pa_extend_tables(t, lens, lens, t.view(-1), i32([1]), lens, i32([0]), slots, lens[:3], i32([0] * (S + 1)))
     torch.cuda.synchronize()
     assert pa.pa_get_device_error() == 0
+
+
+def test_numbers_outside_their_range_are_refused():
+    """Through the extension and, with a stream given, through ctypes."""
+    S, HQ, HKV, D, NB, rnd, cache, i32 = small()
+    k, q = cache(), rnd(S, HQ, D)
+    out = torch.empty((S, HQ, D), device="cuda")
+    t, lens, zero, one = i32([[0, 1]] * S), i32([20] * S), i32([0] * S), i32([1])
+    free, slots, qs = i32([5, 6, 7]), torch.arange(S, device="cuda"), i32([0] * (S + 1))
+    for stream in (None, torch.cuda.current_stream()):
+        for nb in (0, -1, -7):
+            with pytest.raises(pa.PagedAttentionError, match="PA_ERR_INVALID_ARG"):
+                pa.pa_extend_tables(t, lens, zero, free, one, lens, one, slots, zero, qs, num_blocks=nb, stream=stream)
+            with pytest.raises(pa.PagedAttentionError, match="PA_ERR_INVALID_ARG"):
+                pa.pa_release_tables(t, lens, zero, free, one, lens, one, num_blocks=nb, stream=stream)
+        with pytest.raises(pa.PagedAttentionError, match="PA_ERR_INVALID_ARG"):
+            pa.pa_release_tables(t, lens, zero, free, one, lens, one, keep_blocks=-1, stream=stream)
+        for big in (2**31, 2**32 + 5, -2**40):
+            with pytest.raises(OverflowError, match="num_blocks"):
+                pa.pa_extend_tables(t, lens, zero, free, one, lens, one, slots, zero, qs, num_blocks=big, stream=stream)
+            with pytest.raises(OverflowError, match="keep_blocks"):
+                pa.pa_release_tables(t, lens, zero, free, one, lens, one, keep_blocks=big, stream=stream)
+            with pytest.raises(OverflowError, match="max_suffix_len"):
+                pa.pa_decode_shared_prefix(out, q, k, k, t, lens, 32, i32([0, S]), one, 1, 0.1, max_suffix_len=big,
+                                           stream=stream)
+        # numbers of numpy are numbers
+        pa.pa_decode_shared_prefix(out, q, k, k, t, lens, np.int64(32), i32([0, S]), one, np.int32(1), np.float32(0.1),
+                                   max_suffix_len=np.int64(16), k_scale=np.float32(1), stream=stream)
+        pa.pa_release_tables(t, lens, zero, free, one, lens, one, keep_blocks=np.int64(1), num_blocks=np.int32(NB),
+                             stream=stream)
+    torch.cuda.synchronize()
+    assert pa.pa_get_device_error() == 0 and lens.tolist() == [20] * S and one.tolist() == [1]
