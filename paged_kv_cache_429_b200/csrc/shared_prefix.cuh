@@ -81,7 +81,8 @@ struct SharedParams {
   float2 *rec_ml;
 };
 
-__host__ __device__ constexpr int ceil_div(int a, int b) { return (a + b - 1) / b; }
+// (a and b of any size: bounds near 2^31 make a + b pass 32 bits)
+__host__ __device__ constexpr int ceil_div(int a, int b) { return a / b + (a % b != 0); }
 
 // Flags groups that are not ascending inside the batch, and prefixes outside
 // their bound or the table (clamped where they are used). One CTA's threads.

@@ -357,3 +357,13 @@ def test_a_cache_of_more_than_2_to_31_elements():
     assert pa_get_device_error() == 0
     b.k, b.v = small_k, small_v
     b.check(out)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("bound", [2**31 - 1, 2**31 - 130, 2**30])
+def test_loose_bounds_near_32_bits(bound, fp8):
+    """Enough sequences that a suffix is one part, as long as its bound."""
+    b = Batch(8, 8, 64, [100, 28], [3, 2], suffixes(11, 128, 0, 400), fp8=fp8, seed=22)
+    out = b.run(max_len=bound, max_suffix_len=bound)
+    b.check(out)
+    assert pa_get_device_error() == 0
