@@ -247,7 +247,8 @@ PA_API size_t pa_decode_shared_prefix_workspace_size(int num_seqs, int num_q_hea
  * such sequences are better left out of the groups or to pa_decode.
  *   group_start    int32 [num_groups + 1], device, ascending in [0, num_seqs].
  *   prefix_blocks  int32 [num_groups], device; max_prefix_blocks is their
- *                  host-known bound. A value outside [0, max_prefix_blocks]
+ *                  host-known bound (above 8388480, 134 million tokens:
+ *                  PA_ERR_UNSUPPORTED). A value outside [0, max_prefix_blocks]
  *                  or past the table is clamped. PA_DEVERR_GROUP_RANGE flags
  *                  both; sequences of groups that overlap get undefined
  *                  values (nothing faults).

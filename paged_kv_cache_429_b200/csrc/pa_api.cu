@@ -238,7 +238,7 @@ SharedPlan shared_plan(int num_seqs, int num_q_heads, int num_kv_heads, int head
   // waves x (key tiles of a part + 2) smallest; two tiles stand for a CTA's
   // start and its output (four in their place chose the same parts).
   if (s.row_tiles > 0) {
-    const int64_t tiles = (max_prefix_blocks + pa::kSpBlocks - 1) / pa::kSpBlocks;
+    const int64_t tiles = pa::ceil_div(max_prefix_blocks, pa::kSpBlocks);
     const int64_t units = static_cast<int64_t>(s.row_tiles) * num_kv_heads;
     const int64_t least = (tiles + pa::kSpPartTiles - 1) / pa::kSpPartTiles;
     int64_t best = INT64_MAX;
@@ -268,6 +268,9 @@ SharedPlan shared_plan(int num_seqs, int num_q_heads, int num_kv_heads, int head
   s.bytes = s.o_bytes + (rows * 8 + 255) / 256 * 256;
   return s;
 }
+
+// A prefix part is a CTA along grid.z: bounds above 134 million tokens have too many.
+constexpr int kSharedMaxPrefixBlocks = 65535 * pa::kSpPartTiles * pa::kSpBlocks;
 
 // A launch that may start before the stream's kernel in front has finished
 // (the kernel itself waits for it before it reads what that one writes).
@@ -597,8 +600,8 @@ size_t pa_decode_shared_prefix_workspace_size(int num_seqs, int num_q_heads, int
                                               int head_dim, int num_groups, int max_prefix_blocks,
                                               int max_suffix_len) {
   if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || num_groups < 0 ||
-      max_prefix_blocks < 0 || max_suffix_len < 0 || num_q_heads % num_kv_heads != 0 ||
-      num_q_heads / num_kv_heads > 16)
+      max_prefix_blocks < 0 || (num_groups > 0 && max_prefix_blocks > kSharedMaxPrefixBlocks) ||
+      max_suffix_len < 0 || num_q_heads % num_kv_heads != 0 || num_q_heads / num_kv_heads > 16)
     return 0;
   return shared_plan(num_seqs, num_q_heads, num_kv_heads, head_dim, num_groups, max_prefix_blocks,
                      max_suffix_len)
@@ -634,6 +637,7 @@ pa_status pa_decode_shared_prefix(float *out, const void *q, const void *k_cache
   if (num_seqs == 0) return PA_OK;
   if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens)
     return PA_ERR_INVALID_ARG;
+  if (num_groups > 0 && max_prefix_blocks > kSharedMaxPrefixBlocks) return PA_ERR_UNSUPPORTED;
   if (num_groups > 0 && (!group_start || !prefix_blocks)) return PA_ERR_INVALID_ARG;
   if (!aligned(out, 16) || !aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
       !aligned(group_start, 4) || !aligned(prefix_blocks, 4))
@@ -677,7 +681,6 @@ pa_status pa_decode_shared_prefix(float *out, const void *q, const void *k_cache
   if (cudaGetDevice(&dev) != cudaSuccess) return PA_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int rows = static_cast<int>(rows64);
-  if (plan.prefix_parts > 65535) return PA_ERR_UNSUPPORTED;  // grid.z: prefixes above 134 million tokens
   if (head_dim == 128)
     return fp8 ? launch_shared<128, true>(p, k_cache, v_cache, rows, st, dev)
                : launch_shared<128, false>(p, k_cache, v_cache, rows, st, dev);

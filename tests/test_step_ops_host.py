@@ -240,3 +240,21 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
     fused = torch.empty(S, 3 * HQ, D, dtype=bf)
     with pytest.raises(ValueError, match="CUDA device"):  # only its place is wrong
         pa._need_rows(fused[:, HQ:2 * HQ], "key")
+
+
+def test_shared_prefix_bounds_near_32_bits():
+    """Loose bounds up to 2^31 - 1: a suffix bound only makes the parts long,
+    a prefix bound past what a grid holds is refused."""
+    most, limit = 2**31 - 1, 65535 * 128
+    f = _lib.lib().pa_decode_shared_prefix_workspace_size
+    assert f(128, 8, 8, 128, 0, 0, most) == 2 * 128 * 8 * (512 + 8)
+    assert f(1, 8, 8, 128, 1, limit, 16) == (65535 + 1) * 8 * (512 + 8)
+    a = dict(out=FAKE, q=FAKE, k=FAKE, v=FAKE, dtype=0, ks=1.0, vs=1.0, bt=FAKE, maxb=8, cl=FAKE, maxctx=most,
+             gs=FAKE, pb=FAKE, G=1, maxp=limit, maxs=most, S=1, Hq=8, Hkv=8, D=128, B=16, NB=64, scale=0.1, ws=FAKE,
+             wsb=256, stream=None)
+    assert _lib.lib().pa_decode_shared_prefix(*a.values()) == WORKSPACE
+    for maxp in (limit + 1, most - 7, most - 6, most):
+        assert f(1, 8, 8, 128, 1, maxp, 16) == 0
+        a["maxp"] = maxp
+        assert _lib.lib().pa_decode_shared_prefix(*a.values()) == UNSUPPORTED
+        assert f(1, 8, 8, 128, 0, maxp, 16) == 8 * 512 + 256   # without groups it bounds nothing
