@@ -367,3 +367,73 @@ def test_loose_bounds_near_32_bits(bound, fp8):
     out = b.run(max_len=bound, max_suffix_len=bound)
     b.check(out)
     assert pa_get_device_error() == 0
+
+
+def reference(b):
+    """All rows by the formula, in 64 bits on the GPU: (S, Hq, D)."""
+    out = torch.zeros((b.S, b.hq, b.d), dtype=torch.float64, device="cuda")
+    tables = torch.from_numpy(b.tables).cuda().long()
+    for s in range(b.S):
+        n = int(b.lens[s])
+        if n == 0:
+            continue
+        ids = tables[s, :-(-n // B)]
+
+        def rows(t, scale):
+            x = t.view(torch.uint8)[ids].view(torch.float8_e4m3fn) if b.fp8 else t[ids]
+            return x.double().transpose(0, 1).reshape(b.hkv, -1, b.d)[:, :n] * scale
+        z = torch.bmm(b.q[s].double().view(b.hkv, -1, b.d), rows(b.k, b.ks).transpose(1, 2)) * b.scale
+        out[s] = torch.bmm(torch.softmax(z, -1), rows(b.v, b.vs)).reshape(b.hq, b.d)
+    return out
+
+
+def tiles_of_a_part(b):
+    """Key tiles of a part of the longest prefix, from the workspace's size:
+    a record of head_dim values, a maximum and a sum a row and part."""
+    size = lambda g: pa_decode_shared_prefix_workspace_size(b.S, b.hq, b.hkv, b.d, g, int(b.blocks.max()), b.max_suffix)
+    parts = round((size(len(b.blocks)) - size(0)) / (b.S * b.hq * (4 * b.d + 8)))
+    return -(-(-(-int(b.blocks.max()) // 8)) // parts)
+
+
+def slope(b, nats, period, seed):
+    """Scores that rise by `nats` from key tile to key tile of a part, for
+    every other sequence, and fall for the rest: queries +-u plus noise, keys
+    of the prefixes a multiple of u plus noise."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    rnd = lambda *n: torch.randn(n, generator=g, device="cuda")
+    u = torch.where(rnd(b.d) > 0, 1.0, -1.0)
+    sign = torch.where(torch.arange(b.S, device="cuda") % 2 == 0, 1.0, -1.0)[:, None, None]
+    b.q = (sign * u + 0.5 * rnd(b.S, b.hq, b.d)).to(torch.bfloat16)
+    step = nats / (b.d * b.scale)              # of one tile, as a multiple of u
+    b.ks = 0.025 if b.fp8 else 1.0             # the largest key stays below 448 codes
+    for first, n in zip(b.start, b.blocks):
+        ids = torch.from_numpy(b.tables[first, :n]).cuda().long()
+        tile = torch.arange(int(n), device="cuda") // 8 % period
+        x = (tile - (period - 1) / 2)[:, None, None, None] * step * u + 0.5 * rnd(len(ids), b.hkv, B, b.d)
+        assert float(x.abs().max()) / b.ks < (448 if b.fp8 else 1e30)
+        b.k[ids] = (x / b.ks).to(torch.float8_e4m3fn) if b.fp8 else x.to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("nats", [0.0, 0.7, 7.0])
+@pytest.mark.parametrize("hq,hkv,d,sizes,prefixes,tiles", [
+    (32, 32, 64, [150, 140, 10], [320, 313, 47], 14),   # two query tiles and, in the last group, one
+    (32, 32, 128, [40, 3, 1, 128], [320, 200, 9, 320], 14),   # one query tile everywhere
+    (64, 8, 128, [150], [320], 14),                     # eight heads; the last CTA's second tile part full
+    (28, 4, 64, [300], [317], 10),                      # seven heads; a part that ends inside a key tile
+    (32, 32, 128, [260], [256], 16),                    # the longest parts
+])
+def test_parts_of_many_key_tiles(hq, hkv, d, sizes, prefixes, tiles, nats, fp8):
+    """Rings that go round, table entries past the first 32, and scores that
+    pass the running reference again and again (by up to 7 nats, 10 in log2,
+    a tile: far over the 2^15 of E4M3 and, within a part, the 2^60 of bf16)."""
+    b = Batch(hq, hkv, d, sizes, prefixes, suffixes(hq + d, sum(sizes), 0, 30), fp8=fp8, seed=23)
+    assert tiles_of_a_part(b) == tiles
+    if nats:
+        slope(b, nats, tiles, seed=24)
+    out = b.run()
+    torch.cuda.synchronize()
+    assert pa_get_device_error() == 0
+    err = (out.double() - reference(b)).abs()
+    assert bool(torch.isfinite(out).all())
+    assert float(err.max()) <= b.tol(), (float(err.max()), b.tol())
