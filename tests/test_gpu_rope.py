@@ -226,3 +226,44 @@ def test_in_place_other_stream_and_repeat():
     rows = lambda c: c.transpose(1, 2).reshape(-1, 4, 128)[live]
     assert torch.equal(rows(kc), rows(k1)) and torch.equal(vc, v1)
     assert pa_get_device_error() == 0
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("extra,hq,hkv,d,rot,fused", [
+    (0, 2, 1, 64, 64, False),       # the fewest prompt tokens, whole CTAs
+    (1, 7, 1, 128, 128, True),      # one token in the last CTA
+    (2, 5, 5, 64, 48, True),
+    (3, 4, 2, 128, 16, True),
+    (517, 32, 8, 128, 128, True),   # several batches of units a CTA
+])
+def test_prompts_match_the_formula(extra, hq, hkv, d, rot, fused, interleaved, fp8):
+    """From ten tokens an SM on a CTA takes four tokens whole; padding and
+    skipped tokens stand anywhere among them."""
+    T = 10 * torch.cuda.get_device_properties(0).multi_processor_count + extra
+    q, k, v, kc, vc, slots = case(T, hq, hkv, d, T, fp8, fused)
+    slots[T - T // 50:] = -1
+    slots[torch.arange(0, 90, 7, device="cuda")] = -3
+    pos = torch.randint(0, 131072, (T,), device="cuda", dtype=torch.int32,
+                        generator=torch.Generator(device="cuda").manual_seed(T + 1))
+    inv, scale = pa_rope_frequencies(rot, 10000.0, PA_ROPE_YARN, factor=16.0, original_max_position=4096,
+                                     device="cuda")
+    ks, vs = (0.0125, 0.011) if fp8 else (1.0, 1.0)
+    kc0 = kc.clone()
+    vc0 = vc.clone()
+    out = torch.full((T, hq, d), float("nan"), dtype=torch.bfloat16, device="cuda")
+    kw = dict(interleaved=interleaved, rope_scale=scale, k_scale=ks, v_scale=vs)
+    pa_rope_and_cache(out, q, k, v, kc, vc, slots, pos, inv, **kw)
+    torch.cuda.synchronize()
+    check(q, k, v, kc, vc, slots, pos, inv, rot, interleaved, scale, fp8, ks, vs, out, kc0)
+    # in place, and tokens past the pool (one in each place of a CTA) skipped and flagged
+    past = torch.tensor([8, 13, 18, 23], device="cuda")
+    slots[past] = kc.shape[0] * B + past
+    k2, v2, q2 = kc0.clone(), vc0.clone(), q.contiguous().clone()
+    pa_rope_and_cache(q2, q2, k, v, k2, v2, slots, pos, inv, **kw)
+    assert pa_get_device_error() == 0x1 and torch.equal(q2, out)
+    slots[past] = -1
+    k3, v3 = kc0.clone(), vc0.clone()
+    pa_rope_and_cache(q2, q, k, v, k3, v3, slots, pos, inv, **kw)
+    assert np.array_equal(raw(k2), raw(k3)) and np.array_equal(raw(v2), raw(v3))
+    assert pa_get_device_error() == 0
