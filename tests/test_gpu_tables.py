@@ -428,3 +428,90 @@ def test_calls_behind_one_another_see_each_others_results():
     np.testing.assert_array_equal(sl.cpu().numpy(), slots)
     np.testing.assert_array_equal(ps.cpu().numpy(), pos)
     assert int(ct) == count and pa_get_device_error() == 0
+
+
+@pytest.mark.parametrize("inplace", [False, True])
+@pytest.mark.parametrize("what", ["blocks", "row", "tokens", "negative_new", "negative_len", "count_low",
+                                  "count_high", "long_len", "two"])
+def test_large_extends_are_all_or_nothing(what, inplace):
+    """The same refusals where the call is two launches (more than 2048 tokens)."""
+    S, W = 700, 12
+    g, tables, lens, free, count, nb = state(6, S, W, 100, nb_spare=1500)
+    new = np.full(S, 5)
+    T = S * 5 + 9
+    if what in ("blocks", "two"):
+        count = int((-(-(lens + new) // B) - -(-lens // B)).sum()) - 1
+    if what in ("row", "two"):
+        new[699] = W * B - lens[699] + 1
+    if what == "tokens":
+        T = S * 5 - 1
+    elif what == "negative_new":
+        new[350] = -1
+    elif what == "negative_len":
+        lens[0] = -5
+    elif what == "count_low":
+        count = -1
+    elif what == "count_high":
+        count = len(free) + 1
+    elif what == "long_len":
+        lens[7] = 2 ** 31 - 2
+    want = plain_extend(tables, lens, new, free, count, T, nb)
+    assert want[-1] not in (0, BLOCK) and np.all(want[3] == -1)
+    check_extend(run_extend(tables, lens, new, free, count, T, nb, inplace), want)
+
+
+def test_a_large_extend_takes_the_last_block():
+    S, W = 700, 12
+    g, tables, lens, free, count, nb = state(6, S, W, 100, nb_spare=1500)
+    new = np.full(S, 5)
+    need = int((-(-(lens + new) // B) - -(-lens // B)).sum())
+    want = plain_extend(tables, lens, new, free, need, S * 5, nb)
+    assert want[-1] == 0 and want[2] == 0
+    check_extend(run_extend(tables, lens, new, free, need, S * 5, nb), want)
+
+
+def test_a_large_extend_flags_ids_outside_the_pool():
+    S, W = 700, 12
+    g, tables, lens, free, count, nb = state(6, S, W, 100, nb_spare=1500)
+    new = np.full(S, 5)
+    lens[1] = 33
+    tables[1, 2] = nb          # a partly filled block
+    free[count - 2] = -3       # the second block popped
+    want = plain_extend(tables, lens, new, free, count, S * 5 + 1, nb)
+    assert want[-1] == BLOCK
+    check_extend(run_extend(tables, lens, new, free, count, S * 5 + 1, nb), want)
+
+
+@pytest.mark.parametrize("inplace", [False, True])
+@pytest.mark.parametrize("what", ["full", "count_low", "count_high", "length", "negative", "bad_id", "fits"])
+def test_large_releases_refuse_on_the_device(what, inplace):
+    """Where the call is two launches (a bound of more than 8192 blocks)."""
+    S, W = 700, 14
+    g, tables, lens, free, count, nb = state(14, S, W, W * B)
+    lens[3] = 77
+    rel = (g.random(S) < 0.9).astype(np.int64)
+    rel[[3, 699]] = 1
+    held = int(sum(-(-int(a) // B) for a, r in zip(lens, rel) if r))
+    if what in ("full", "fits"):
+        free = free[:count + held - (what == "full")]
+    elif what == "count_low":
+        count = -2
+    elif what == "count_high":
+        count = len(free) + 1
+    elif what == "length":
+        lens[699] = W * B + 1
+    elif what == "negative":
+        lens[3] = -1
+    elif what == "bad_id":
+        tables[3, 1] = nb + 4
+    fr, ln, ct = dev(free), dev(lens), dev([count])
+    lo = ln if inplace else torch.full_like(ln, -9)
+    co = ct if inplace else torch.full_like(ct, -9)
+    pa_release_tables(dev(tables), ln, dev(rel), fr, ct, lo, co, num_blocks=nb)
+    torch.cuda.synchronize()
+    wf, wl, wc, flags = plain_release(tables, lens, rel, free, count, 0, nb)
+    assert (flags != 0) == (what != "fits")
+    np.testing.assert_array_equal(fr.cpu().numpy(), wf)
+    np.testing.assert_array_equal(lo.cpu().numpy(), wl)
+    assert int(co) == wc
+    assert pa_get_device_error() == flags
