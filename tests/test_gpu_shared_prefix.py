@@ -437,3 +437,43 @@ def test_parts_of_many_key_tiles(hq, hkv, d, sizes, prefixes, tiles, nats, fp8):
     err = (out.double() - reference(b)).abs()
     assert bool(torch.isfinite(out).all())
     assert float(err.max()) <= b.tol(), (float(err.max()), b.tol())
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("groups", [31, 32, 33, 64, 65, 100, 1100])
+def test_more_groups_than_a_warp(groups, fp8):
+    """Parallel samples: groups of 0 to 4 sequences, some without a prefix,
+    and sequences of no group behind them."""
+    g = np.random.default_rng(groups)
+    sizes = g.integers(0, 5 if groups < 1000 else 2, groups)
+    sizes[[0, groups - 1]] = [2, 3]
+    prefixes = g.integers(0, 13, groups)
+    b = Batch(8, 2, 64, list(sizes), list(prefixes), suffixes(groups, int(sizes.sum()) + 5, 0, 40), fp8=fp8, seed=25,
+              tail=5)
+    out = b.run()
+    torch.cuda.synchronize()
+    b.check(out)
+    assert pa_get_device_error() == 0
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_clamped_groups_give_the_same_values(fp8):
+    """Prefixes outside their bound are clamped, a group that passes the
+    batch's ends is cut there: every sequence still attends to its context."""
+    b = Batch(8, 4, 64, [3, 3, 3], [3, 3, 3], suffixes(26, 9, 1, 60), fp8=fp8, seed=26)
+    for start, blocks, suffix in (([0, 3, 6, 9], [3, -2, 1000], 3 * B + b.max_suffix),
+                                  ([-5, 3, 6, 100], [3, 3, 3], b.max_suffix)):
+        out = b.run(start=np.array(start), blocks=np.array(blocks), max_prefix=3, max_suffix_len=suffix)
+        torch.cuda.synchronize()
+        assert pa_get_device_error() == GROUP
+        b.check(out)
+
+
+def test_sequences_beside_overlapping_groups_are_right():
+    """[3, 7), [7, 5) and [5, 9) overlap, which is flagged; the group in front
+    of them and the sequences of no group keep their values."""
+    b = Batch(8, 4, 64, [3, 6], [4, 3], suffixes(27, 12, 1, 60), seed=27, tail=3)
+    out = b.run(start=np.array([0, 3, 7, 5, 9]), blocks=np.array([4, 3, 3, 3]))
+    torch.cuda.synchronize()
+    assert pa_get_device_error() & GROUP
+    b.check(out, subset=np.array([0, 1, 2, 9, 10, 11]))
