@@ -370,8 +370,9 @@ PA_API pa_status pa_rope_frequencies(double *inv_freq_out, float *rope_scale_out
  * pass through. For token t and theta = positions[t] * inv_freq[i]:
  *     (a, b) -> rope_scale * (a cos theta - b sin theta,
  *                             b cos theta + a sin theta)
- * in fp32 with the angle reduced exactly (any int32 position keeps full
- * precision), rounded once: q_out to bf16, keys to the cache type. Values
+ * in fp32, the angle off by less than 2^-23 + 2^-104 |theta| radians (so any
+ * int32 position keeps fp32's precision, far beyond any frequency in use),
+ * rounded once: q_out to bf16, keys to the cache type. Values
  * and unrotated key elements are stored as pa_reshape_and_cache stores them.
  *   q_out          bf16 [num_tokens][num_q_heads][head_dim], 16-byte aligned.
  *                  May be q itself when q_stride = num_q_heads * head_dim;

@@ -14,9 +14,12 @@
 // radians at position 131072, more than bf16 resolves. Only the fraction of
 // a turn matters, so inv_freq / 2 pi is held as a 64-bit fixed-point
 // fraction of a turn, F = round(2^64 frac(inv_freq / 2 pi)), and
-// t * F mod 2^64 — one integer product that wraps — is the exact fraction
-// of the turn; its high word as a float (2^-25 of a half turn) goes to
-// sincospi.
+// t * F mod 2^64 is one integer product that wraps; its high word as a float
+// (2^-25 of a half turn) goes to sincospi. The product multiplies F's own
+// error by t, so F is formed from inv_freq / 2 pi in two doubles (off by
+// 2^-105 of it) and is off by one unit of 2^-64 turns: at 2^31, 2^-33 turns.
+// One double would leave 2^-53 of the angle, 2e-5 radians for 100 at 2^31.
+// Together below 2^-23 radians + 2^-104 |t inv_freq|.
 //
 // What bounds it: DRAM for prompts (32768 tokens of 32 query and 8 KV heads
 // of 128, 806 MB, in 132 us: 0.93 of the copy bandwidth), the latency of a
@@ -61,10 +64,14 @@ struct RopeParams {
 
 // cosine and sine of position * inv_freq (see the head comment), times scale
 __device__ __forceinline__ float2 rope_cos_sin(int position, double inv_freq, float scale) {
-  double turn = inv_freq * 0.15915494309189533577;  // 1 / 2 pi
-  turn -= rint(turn);
-  const int64_t f = __double2ll_rn(turn * 18446744073709551616.0);
-  const uint64_t a = static_cast<uint64_t>(static_cast<int64_t>(position)) * static_cast<uint64_t>(f);
+  constexpr double kHi = 0.15915494309189535, kLo = -9.839338337591243e-18;  // 1 / 2 pi
+  double hi = inv_freq * kHi;
+  double lo = fma(inv_freq, kLo, fma(inv_freq, kHi, -hi));
+  hi -= rint(hi);
+  lo -= rint(lo);
+  constexpr double kUnits = 18446744073709551616.0;
+  const uint64_t f = static_cast<uint64_t>(__double2ll_rn(hi * kUnits)) + static_cast<uint64_t>(__double2ll_rn(lo * kUnits));
+  const uint64_t a = static_cast<uint64_t>(static_cast<int64_t>(position)) * f;
   const float half_turns = static_cast<float>(static_cast<int32_t>(a >> 32)) * 4.656612873077393e-10f;
   float s, c;
   sincospif(half_turns, &s, &c);

@@ -267,3 +267,24 @@ def test_prompts_match_the_formula(extra, hq, hkv, d, rot, fused, interleaved, f
     pa_rope_and_cache(q2, q, k, v, k3, v3, slots, pos, inv, **kw)
     assert np.array_equal(raw(k2), raw(k3)) and np.array_equal(raw(v2), raw(v3))
     assert pa_get_device_error() == 0
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_large_frequencies_at_far_positions(interleaved):
+    """The product is reduced with the frequency's full 53 bits and both of
+    1 / 2 pi's doubles: 2^-104 of an angle of up to 2^62 radians, far below the
+    tolerance's 2^-20."""
+    inv = torch.tensor([1.0, -7.5, 100.0, 12345.678, -1e6, 2.0 ** 31 + 0.37, 3e-7, 3.14159265], dtype=torch.float64,
+                       device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(5)
+    far = torch.randint(-2 ** 31, 2 ** 31, (190,), device="cuda", generator=g).to(torch.int32)
+    ends = torch.tensor([-2 ** 31, 2 ** 31 - 1, -2 ** 31 + 1, 2 ** 30, -2 ** 30, 131071, 1, 0, -1, 2 ** 24 + 1],
+                        dtype=torch.int32, device="cuda")
+    pos = torch.cat([far, ends])
+    T = len(pos)
+    q, k, v, kc, vc, slots = case(T, 4, 2, 64, 51, False, True)
+    kc0 = kc.clone()
+    out = torch.empty((T, 4, 64), dtype=torch.bfloat16, device="cuda")
+    pa_rope_and_cache(out, q, k, v, kc, vc, slots, pos, inv, interleaved=interleaved)
+    torch.cuda.synchronize()
+    check(q, k, v, kc, vc, slots, pos, inv, 16, interleaved, 1.0, False, 1.0, 1.0, out, kc0)
