@@ -417,9 +417,13 @@ def pa_reshape_and_cache(key: torch.Tensor, value: torch.Tensor,
 
 def pa_rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: int = PA_ROPE_NONE, *,
                         factor: float = 1.0, original_max_position: float = 0.0,
-                        low: float = 1.0, high: float = 32.0, device=None):
+                        low: float = 1.0, high: Optional[float] = None, device=None):
     """The frequency table of pa_rope_and_cache (see pa.h for the scalings):
-    (inv_freq fp64 [rotary_dim / 2] on `device`, rope_scale)."""
+    (inv_freq fp64 [rotary_dim / 2] on `device`, rope_scale). high: the turns
+    in the original context from which a component is kept (default: 4 for
+    PA_ROPE_BANDS, 32 for PA_ROPE_YARN, the bounds those are used with)."""
+    if high is None:
+        high = 4.0 if scaling == PA_ROPE_BANDS else 32.0
     inv = torch.empty(max(int(rotary_dim), 0) // 2, dtype=torch.float64)
     scale = ctypes.c_float(0.0)
     _ok(_lib.lib().pa_rope_frequencies(inv.data_ptr() or None, ctypes.byref(scale), int(rotary_dim),

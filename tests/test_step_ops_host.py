@@ -258,3 +258,14 @@ def test_shared_prefix_bounds_near_32_bits():
         a["maxp"] = maxp
         assert _lib.lib().pa_decode_shared_prefix(*a.values()) == UNSUPPORTED
         assert f(1, 8, 8, 128, 0, maxp, 16) == 8 * 512 + 256   # without groups it bounds nothing
+
+
+@pytest.mark.parametrize("scaling,high", [(pa.PA_ROPE_BANDS, 4.0), (pa.PA_ROPE_YARN, 32.0)])
+def test_the_upper_bound_goes_by_the_scaling(scaling, high):
+    kw = dict(factor=8.0, original_max_position=8192)
+    inv, scale = pa.pa_rope_frequencies(128, 500000.0, scaling, **kw)
+    want, want_scale = plain_frequencies(128, 500000.0, scaling, 8.0, 8192, 1.0, high)
+    np.testing.assert_allclose(inv.numpy(), want, rtol=1e-14, atol=0)
+    assert scale == pytest.approx(want_scale, rel=2 ** -23)
+    given, _ = pa.pa_rope_frequencies(128, 500000.0, scaling, high=high, **kw)
+    assert torch.equal(inv, given)
