@@ -116,7 +116,7 @@ def _check_all(tensors, specs) -> int:
         dev = tensors[0].get_device()
         for t, (_, dtypes, ndim) in zip(tensors, specs):
             if (t.get_device() != dev or t.dim() != ndim or t.dtype not in dtypes
-                    or not t.is_contiguous()):
+                    or not t.is_contiguous() or max(t.shape) >= 2**31):
                 break
         else:
             if dev >= 0:
@@ -125,6 +125,8 @@ def _check_all(tensors, specs) -> int:
         pass
     for t, (name, dtypes, ndim) in zip(tensors, specs):
         _need(t, name, dtypes, ndim)
+        for n in t.shape:
+            _int32(n, name)
     return _device_of(*tensors).index
 
 
@@ -294,8 +296,10 @@ def pa_decode_shared_prefix_workspace_size(num_seqs: int, num_q_heads: int, num_
                                            head_dim: int, num_groups: int, max_prefix_blocks: int,
                                            max_suffix_len: int) -> int:
     return int(_lib.lib().pa_decode_shared_prefix_workspace_size(
-        num_seqs, num_q_heads, num_kv_heads, head_dim, num_groups, max_prefix_blocks,
-        max_suffix_len))
+        _int32(num_seqs, "num_seqs"), _int32(num_q_heads, "num_q_heads"),
+        _int32(num_kv_heads, "num_kv_heads"), _int32(head_dim, "head_dim"),
+        _int32(num_groups, "num_groups"), _int32(max_prefix_blocks, "max_prefix_blocks"),
+        _int32(max_suffix_len, "max_suffix_len")))
 
 
 def pa_decode_shared_prefix(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
@@ -424,10 +428,11 @@ def pa_rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: int = P
     PA_ROPE_BANDS, 32 for PA_ROPE_YARN, the bounds those are used with)."""
     if high is None:
         high = 4.0 if scaling == PA_ROPE_BANDS else 32.0
-    inv = torch.empty(max(int(rotary_dim), 0) // 2, dtype=torch.float64)
+    rotary_dim, scaling = _int32(rotary_dim, "rotary_dim"), _int32(scaling, "scaling")
+    inv = torch.empty(max(rotary_dim, 0) // 2, dtype=torch.float64)
     scale = ctypes.c_float(0.0)
-    _ok(_lib.lib().pa_rope_frequencies(inv.data_ptr() or None, ctypes.byref(scale), int(rotary_dim),
-                                       float(base), int(scaling), float(factor),
+    _ok(_lib.lib().pa_rope_frequencies(inv.data_ptr() or None, ctypes.byref(scale), rotary_dim,
+                                       float(base), scaling, float(factor),
                                        float(original_max_position), float(low), float(high)),
         "pa_rope_frequencies")
     return (inv if device is None else inv.to(device)), float(scale.value)

@@ -33,6 +33,7 @@ struct Call {
     }
     const at::Tensor &t = THPVariable_Unpack(args[i]);
     if (!t.defined() || !t.is_cuda() || t.dim() != dims || (contiguous && !t.is_contiguous())) fine = false;
+    for (const int64_t n : t.sizes()) fine = fine && n <= INT32_MAX;  // sizes are passed as int
     if (fine && device < 0) device = t.get_device();
     if (fine && t.get_device() != device) fine = false;
     return fine ? &t : &none;
@@ -113,7 +114,6 @@ T *ptr(const at::Tensor *t) {
   return static_cast<T *>(t->data_ptr());
 }
 int len(const at::Tensor *t, int d) { return static_cast<int>(t->size(d)); }
-bool small(const at::Tensor *t) { return t->numel() <= INT32_MAX; }
 
 // (block_tables, context_lens, new_lens, free_blocks, free_count,
 // context_lens_out, free_count_out, slot_mapping, positions, query_start,
@@ -127,7 +127,7 @@ PyObject *extend_tables(PyObject *const *args, Py_ssize_t n) {
                    *slots = c.typed(7, 1, at::kLong), *pos = c.typed(8, 1, at::kInt), *qs = c.typed(9, 1, at::kInt);
   const bool whole = args[10] == Py_None;  // the pool is as large as the stack
   int nb = whole ? 0 : c.integer(10);
-  if (!c.ready() || !small(slots) || !small(free)) Py_RETURN_NONE;
+  if (!c.ready()) Py_RETURN_NONE;
   const int64_t S = bt->size(0);
   if (lens->size(0) != S || more->size(0) != S || lens_out->size(0) != S || count->size(0) != 1 ||
       count_out->size(0) != 1 || pos->size(0) != slots->size(0) || qs->size(0) != S + 1)
@@ -152,7 +152,7 @@ PyObject *release_tables(PyObject *const *args, Py_ssize_t n) {
   const int keep = c.integer(7);
   const bool whole = args[8] == Py_None;
   int nb = whole ? 0 : c.integer(8);
-  if (!c.ready() || !small(free)) Py_RETURN_NONE;
+  if (!c.ready()) Py_RETURN_NONE;
   const int64_t S = bt->size(0);
   if (lens->size(0) != S || rel->size(0) != S || lens_out->size(0) != S || count->size(0) != 1 ||
       count_out->size(0) != 1)
@@ -181,7 +181,7 @@ PyObject *rope_and_cache(PyObject *const *args, Py_ssize_t n) {
     PyErr_Clear();
     Py_RETURN_NONE;
   }
-  if (!c.ready() || !small(slots)) Py_RETURN_NONE;
+  if (!c.ready()) Py_RETURN_NONE;
   const int64_t T = q->size(0), D = q->size(2), Hkv = kc->size(1);
   if (out->sizes() != q->sizes() || kc->size(3) != D || vc->sizes() != kc->sizes() ||
       vc->scalar_type() != kc->scalar_type() || k->size(0) != T || k->size(1) != Hkv || k->size(2) != D ||

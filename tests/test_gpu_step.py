@@ -298,3 +298,25 @@ def test_numbers_outside_their_range_are_refused():
                              stream=stream)
     torch.cuda.synchronize()
     assert pa.pa_get_device_error() == 0 and lens.tolist() == [20] * S and one.tolist() == [1]
+
+
+def test_tensors_of_more_than_2_to_31_columns_are_refused():
+    """A table of 2^32 + 8 columns is not one of 8."""
+    S, HQ, HKV, D, NB, rnd, cache, i32 = small()
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 17 GB of device memory")
+    k, q = cache(), rnd(1, HQ, D)
+    out = torch.empty((1, HQ, D), device="cuda")
+    wide = torch.empty((1, 2**32 + 8), dtype=torch.int32, device="cuda")
+    lens, zero, one = i32([20]), i32([0]), i32([1])
+    free, slots, qs = i32([5, 6, 7]), torch.arange(1, device="cuda"), i32([0, 0])
+    for stream in (None, torch.cuda.current_stream()):
+        with pytest.raises(OverflowError, match="block_tables"):
+            pa.pa_extend_tables(wide, lens, zero, free, one, lens, one, slots, zero, qs, num_blocks=NB, stream=stream)
+        with pytest.raises(OverflowError, match="block_tables"):
+            pa.pa_release_tables(wide, lens, zero, free, one, lens, one, num_blocks=NB, stream=stream)
+        with pytest.raises(OverflowError, match="block_tables"):
+            pa.pa_decode_shared_prefix(out, q, k, k, wide, lens, 32, i32([0, 1]), one, 1, 0.1, max_suffix_len=32,
+                                       stream=stream)
+    torch.cuda.synchronize()
+    assert pa.pa_get_device_error() == 0

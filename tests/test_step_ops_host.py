@@ -269,3 +269,19 @@ def test_the_upper_bound_goes_by_the_scaling(scaling, high):
     assert scale == pytest.approx(want_scale, rel=2 ** -23)
     given, _ = pa.pa_rope_frequencies(128, 500000.0, scaling, high=high, **kw)
     assert torch.equal(inv, given)
+
+
+@pytest.mark.parametrize("big", [2**31, 2**32 + 64, -2**31 - 1])
+def test_sizes_past_32_bits_raise(big):
+    """Nothing is cut to its lower 32 bits on the way into the library."""
+    with pytest.raises(OverflowError, match="rotary_dim"):
+        pa.pa_rope_frequencies(big)
+    with pytest.raises(OverflowError, match="scaling"):
+        pa.pa_rope_frequencies(64, 10000.0, big)
+    names = ("num_seqs", "num_q_heads", "num_kv_heads", "head_dim", "num_groups", "max_prefix_blocks",
+             "max_suffix_len")
+    for i, name in enumerate(names):
+        a = [4, 8, 8, 64, 1, 4, 100]
+        a[i] = big
+        with pytest.raises(OverflowError, match=name):
+            pa.pa_decode_shared_prefix_workspace_size(*a)
