@@ -259,7 +259,8 @@ PA_API size_t pa_decode_shared_prefix_workspace_size(int num_seqs, int num_q_hea
  *   workspace      pa_decode_shared_prefix_workspace_size(...) bytes, 256-byte
  *                  aligned, else PA_ERR_WORKSPACE; two calls that may run at
  *                  the same time need one each.
- *   Other arguments as for pa_decode; caches of both types. */
+ *   Other arguments as for pa_decode (the int32 arrays 4-byte aligned);
+ *   caches of both types. */
 PA_API pa_status pa_decode_shared_prefix(float *out, const void *q, const void *k_cache,
                                          const void *v_cache, pa_kv_dtype kv_dtype,
                                          float k_scale, float v_scale,
@@ -386,7 +387,8 @@ PA_API pa_status pa_rope_frequencies(double *inv_freq_out, float *rope_scale_out
  *                  rotated and nothing cached.
  *                  Slots of different tokens differ (where two tokens have
  *                  one slot, each element stored is either's).
- *   positions      int32 [num_tokens], device; any value.
+ *   positions      int32 [num_tokens], device; any value (4-byte aligned,
+ *                  slot_mapping 8-byte).
  *   inv_freq       fp64 [rotary_dim / 2], device, finite (8-byte aligned).
  *   rotary_dim     a multiple of 16 in [16, head_dim]; others return
  *                  PA_ERR_UNSUPPORTED.

@@ -640,7 +640,8 @@ pa_status pa_decode_shared_prefix(float *out, const void *q, const void *k_cache
   if (num_groups > 0 && max_prefix_blocks > kSharedMaxPrefixBlocks) return PA_ERR_UNSUPPORTED;
   if (num_groups > 0 && (!group_start || !prefix_blocks)) return PA_ERR_INVALID_ARG;
   if (!aligned(out, 16) || !aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
-      !aligned(group_start, 4) || !aligned(prefix_blocks, 4))
+      !aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(group_start, 4) ||
+      !aligned(prefix_blocks, 4))
     return PA_ERR_INVALID_ARG;
   const int64_t rows64 = static_cast<int64_t>(num_blocks) * num_kv_heads * pa::kBS;
   if (rows64 + pa::kBS >= INT32_MAX) return PA_ERR_UNSUPPORTED;
@@ -867,7 +868,8 @@ pa_status pa_rope_and_cache(void *q_out, const void *q, const void *key, const v
   if (!q_out || !q || !key || !value || !k_cache || !v_cache || !slot_mapping || !positions || !inv_freq)
     return PA_ERR_INVALID_ARG;
   if (!aligned(q_out, 16) || !aligned(q, 16) || !aligned(key, 16) || !aligned(value, 16) ||
-      !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(inv_freq, 8))
+      !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(slot_mapping, 8) ||
+      !aligned(positions, 4) || !aligned(inv_freq, 8))
     return PA_ERR_INVALID_ARG;
   if (q_out == q && q_stride != q_row) return PA_ERR_INVALID_ARG;
   pa::RopeParams p{};

@@ -285,3 +285,21 @@ def test_sizes_past_32_bits_raise(big):
         a[i] = big
         with pytest.raises(OverflowError, match=name):
             pa.pa_decode_shared_prefix_workspace_size(*a)
+
+
+@pytest.mark.parametrize("kw", [dict(slots=FAKE + 4), dict(slots=FAKE + 1), dict(pos=FAKE + 2)])
+def test_rope_rejects_misaligned_arrays(kw):
+    a = dict(q_out=FAKE + 0x100000, q=FAKE, key=FAKE, value=FAKE, k=FAKE, v=FAKE, slots=FAKE, pos=FAKE, inv=FAKE,
+             rot=128, il=0, scale=1.0, qs=1024, ks=1024, vs_=1024, T=4, Hq=8, Hkv=8, D=128, B=16, NB=64, dtype=0,
+             ksc=1.0, vsc=1.0, stream=None)
+    a.update(kw)
+    assert _lib.lib().pa_rope_and_cache(*a.values()) == INVALID
+
+
+@pytest.mark.parametrize("kw", [dict(bt=FAKE + 2), dict(cl=FAKE + 1), dict(gs=FAKE + 2), dict(pb=FAKE + 3)])
+def test_shared_prefix_rejects_misaligned_arrays(kw):
+    a = dict(out=FAKE, q=FAKE, k=FAKE, v=FAKE, dtype=0, ks=1.0, vs=1.0, bt=FAKE, maxb=8, cl=FAKE, maxctx=128,
+             gs=FAKE, pb=FAKE, G=1, maxp=4, maxs=64, S=2, Hq=8, Hkv=8, D=128, B=16, NB=64, scale=0.1, ws=None, wsb=0,
+             stream=None)
+    a.update(kw)
+    assert _lib.lib().pa_decode_shared_prefix(*a.values()) == INVALID
