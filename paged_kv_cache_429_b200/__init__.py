@@ -130,6 +130,17 @@ def _check_all(tensors, specs) -> int:
     return _device_of(*tensors).index
 
 
+def _need_workspace(t: torch.Tensor, dev: int) -> None:
+    """A caller's workspace: its elements are its bytes only where they follow
+    one another (an expanded tensor holds fewer than it has)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
+    if not t.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    if t.get_device() != dev:
+        raise ValueError("the workspace must be on the device of the call's tensors")
+
+
 def _call(what: str, dev: int, *args) -> None:
     """One launching entry point with device `dev` current."""
     fn = getattr(_lib.lib(), what)
@@ -349,8 +360,8 @@ def pa_decode_shared_prefix(out: torch.Tensor, q: torch.Tensor, k_cache: torch.T
         else:
             with torch.cuda.stream(stream):
                 workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-    elif workspace.get_device() != dev:
-        raise ValueError("the workspace must be on the device of the call's tensors")
+    else:
+        _need_workspace(workspace, dev)
     _call("pa_decode_shared_prefix", dev,
           out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
           kv_dtype_of(k_cache), float(k_scale), float(v_scale), block_tables.data_ptr(), block_tables.shape[1],

@@ -320,3 +320,15 @@ def test_tensors_of_more_than_2_to_31_columns_are_refused():
                                        stream=stream)
     torch.cuda.synchronize()
     assert pa.pa_get_device_error() == 0
+
+
+def test_an_expanded_workspace_is_refused():
+    S, HQ, HKV, D, NB, rnd, cache, i32 = small()
+    k, q = cache(), rnd(S, HQ, D)
+    out = torch.full((S, HQ, D), 7.0, device="cuda")
+    ws = torch.empty(256, dtype=torch.uint8, device="cuda")
+    for bad in (ws[:1].expand(1 << 20), torch.empty((1 << 20, 2), dtype=torch.uint8, device="cuda")[:, 0], ws.cpu()):
+        with pytest.raises(ValueError, match="workspace"):
+            pa.pa_decode_shared_prefix(out, q, k, k, i32([[0, 1]] * S), i32([20] * S), 32, i32([0, S]), i32([1]), 1, 0.1,
+                                       max_suffix_len=16, workspace=bad)
+    assert torch.all(out == 7.0)

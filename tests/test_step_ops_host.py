@@ -303,3 +303,15 @@ def test_shared_prefix_rejects_misaligned_arrays(kw):
              stream=None)
     a.update(kw)
     assert _lib.lib().pa_decode_shared_prefix(*a.values()) == INVALID
+
+
+def test_binding_refuses_workspaces_that_hold_less_than_they_say():
+    with pytest.raises(ValueError, match="contiguous"):
+        pa._need_workspace(torch.empty(1, dtype=torch.uint8).expand(1 << 20), -1)
+    with pytest.raises(ValueError, match="contiguous"):
+        pa._need_workspace(torch.empty(512, 2, dtype=torch.uint8)[:, 0], -1)
+    with pytest.raises(ValueError, match="device"):
+        pa._need_workspace(torch.empty(512, dtype=torch.uint8), 0)
+    with pytest.raises(TypeError, match="torch.Tensor"):
+        pa._need_workspace(np.empty(512, np.uint8), 0)
+    pa._need_workspace(torch.empty(512, dtype=torch.uint8), -1)
