@@ -163,6 +163,9 @@ class DecodeBatch:
                 b._dev_slots[id(op)] = torch.from_numpy(op.slots).to(dev)
             else:
                 b._dev_pairs[id(op)] = torch.from_numpy(op.pairs).to(dev)
+        # the batch as one group behind its prefix (step_shared)
+        b._group_start = torch.tensor([0, S], dtype=torch.int32, device=dev)
+        b._prefix_blocks = torch.tensor([w.prefix_len // BS], dtype=torch.int32, device=dev)
         b.out = torch.empty((S, Hq, D), dtype=torch.float32, device=dev)
         b.run_ops(b.setup_ops)
         return b
@@ -204,10 +207,6 @@ class DecodeBatch:
         prefix (pa_decode_shared_prefix): the prefix's full blocks are read
         and multiplied once for all sequences. A batch without a prefix is a
         group whose sequences share nothing."""
-        if not hasattr(self, "_group_start"):
-            blocks = self.w.prefix_len // BS
-            self._group_start = torch.tensor([0, self.w.num_seqs], dtype=torch.int32, device=self.device)
-            self._prefix_blocks = torch.tensor([blocks], dtype=torch.int32, device=self.device)
         blocks = self.w.prefix_len // BS
         self.run_ops(self.step_ops, stream=stream)
         return pa_decode_shared_prefix(self.out, self.q, self.k_cache, self.v_cache,

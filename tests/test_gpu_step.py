@@ -332,3 +332,20 @@ def test_an_expanded_workspace_is_refused():
             pa.pa_decode_shared_prefix(out, q, k, k, i32([[0, 1]] * S), i32([20] * S), 32, i32([0, S]), i32([1]), 1, 0.1,
                                        max_suffix_len=16, workspace=bad)
     assert torch.all(out == 7.0)
+
+
+def test_a_new_batch_is_captured_at_its_first_step_shared():
+    warm = DecodeBatch.build(synth.WORKLOADS["tiny"], 3, "cuda:0")
+    want = warm.step_shared().clone()      # loads the kernels, and says what comes out
+    b = DecodeBatch.build(synth.WORKLOADS["tiny"], 3, "cuda:0")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        b.step_shared()
+    for _ in range(2):
+        b.out.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(b.out, want)
+    assert pa.pa_get_device_error() == 0
+    del graph
