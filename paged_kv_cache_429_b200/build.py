@@ -26,6 +26,7 @@ DEPS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC)
 BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
 BINDING = os.path.join(HERE, "_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
 BINDING_DEPS = [BINDING_SOURCE, os.path.join(INCLUDE, "pa.h")]
+BINDING_STAMP = os.path.join(HERE, "_build", "binding.txt")  # the torch it was built with
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -51,9 +52,22 @@ def up_to_date() -> bool:
     return _newer(LIB, DEPS)
 
 
+def _torch_id() -> str:
+    import torch
+    return f"torch {torch.__version__} abi {int(torch._C._GLIBCXX_USE_CXX11_ABI)}\n"
+
+
+def binding_up_to_date() -> bool:
+    """Newer than its sources, and built with the torch that is here now."""
+    if not _newer(BINDING, BINDING_DEPS) or not os.path.exists(BINDING_STAMP):
+        return False
+    with open(BINDING_STAMP) as f:
+        return f.read() == _torch_id()
+
+
 def build_binding(force: bool = False) -> str:
     """The extension links libpa.so next to it, and the torch it is run with."""
-    if not force and _newer(BINDING, BINDING_DEPS):
+    if not force and binding_up_to_date():
         return BINDING
     import torch
     troot = os.path.dirname(torch.__file__)
@@ -67,7 +81,12 @@ def build_binding(force: bool = False) -> str:
         cmd += ["-isystem" if d is not INCLUDE else "-I", d]
     cmd += ["-o", BINDING, BINDING_SOURCE, "-L", HERE, "-lpa", "-L", os.path.join(troot, "lib"),
             "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+    if os.path.exists(BINDING_STAMP):
+        os.remove(BINDING_STAMP)
     subprocess.run(cmd, check=True)
+    os.makedirs(os.path.dirname(BINDING_STAMP), exist_ok=True)
+    with open(BINDING_STAMP, "w") as f:
+        f.write(_torch_id())
     return BINDING
 
 
