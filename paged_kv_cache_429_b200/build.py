@@ -3,7 +3,8 @@ _binding, the Python extension in front of it (csrc/binding.cpp).
 
 Usage: ``python -m paged_kv_cache_429_b200.build`` (or via
 ``__graft_entry__.build()``). The library is written next to this file so it
-travels with the source tree.
+travels with the source tree. ``--library`` builds libpa.so alone, for callers
+of the C ABI: the extension also needs Python's and torch's headers.
 """
 from __future__ import annotations
 
@@ -90,19 +91,22 @@ def build_binding(force: bool = False) -> str:
     return BINDING
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
+def build(force: bool = False, verbose: bool = False, binding: bool = True) -> str:
+    """libpa.so and, unless `binding` is false, the extension in front of it."""
     if not force and up_to_date():
-        build_binding()
+        if binding:
+            build_binding()
         return LIB
     cmd = [_nvcc(), *NVCC_FLAGS, "-I", INCLUDE, "-I", CSRC, "-o", LIB, *SOURCES]
     if verbose:
         cmd.insert(1, "-Xptxas=-v")
         print(" ".join(cmd), file=sys.stderr)
     subprocess.run(cmd, check=True)
-    build_binding(force)
+    if binding:
+        build_binding(force)
     return LIB
 
 
 if __name__ == "__main__":
-    build(force="--force" in sys.argv, verbose="-v" in sys.argv)
+    build(force="--force" in sys.argv, verbose="-v" in sys.argv, binding="--library" not in sys.argv)
     print(LIB)

@@ -59,3 +59,15 @@ def test_a_build_that_fails_leaves_no_mark(tree, monkeypatch):
             build.build_binding(force=True)
     build.build_binding()
     assert len(runs) == 2
+
+
+def test_the_library_alone_needs_no_extension(tree, tmp_path, monkeypatch):
+    src, so, runs = tree
+    monkeypatch.setattr(build, "LIB", str(tmp_path / "libpa.so"))
+    build.build(force=True, binding=False)
+    assert len(runs) == 1 and not any("binding.cpp" in a for a in runs[0])
+    monkeypatch.setattr(build, "up_to_date", lambda: True)
+    build.build(binding=False)
+    assert len(runs) == 1
+    build.build()
+    assert len(runs) == 2
