@@ -81,8 +81,10 @@ struct SharedParams {
   float2 *rec_ml;
 };
 
-// (a and b of any size: bounds near 2^31 make a + b pass 32 bits)
-__host__ __device__ constexpr int ceil_div(int a, int b) { return a / b + (a % b != 0); }
+// (unsigned: with bounds near 2^31, a + b passes a signed 32-bit sum)
+__host__ __device__ constexpr int ceil_div(int a, int b) {
+  return static_cast<int>((static_cast<uint32_t>(a) + static_cast<uint32_t>(b) - 1u) / static_cast<uint32_t>(b));
+}
 
 // Flags groups that are not ascending inside the batch, and prefixes outside
 // their bound or the table (clamped where they are used). One CTA's threads.
