@@ -354,8 +354,8 @@ typedef enum {
 /* The table pa_rope_and_cache reads: inv_freq_out fp64 [rotary_dim / 2]
  * (HOST) receives the angles per position in radians, *rope_scale_out (host)
  * the factor on the rotated values (1 except for PA_ROPE_YARN). rotary_dim:
- * a positive even number (above 2 for PA_ROPE_BASE); base > 1; factor >= 1
- * (not read for NONE); original_max_position > 0 and 0 < low < high for
+ * a positive even number (above 2 for PA_ROPE_BASE, whose stretched base has
+ * to be finite); base > 1; factor >= 1 (not read for NONE); original_max_position > 0 and 0 < low < high for
  * BANDS and YARN (not read otherwise). Anything else: PA_ERR_INVALID_ARG. */
 PA_API pa_status pa_rope_frequencies(double *inv_freq_out, float *rope_scale_out,
                                      int rotary_dim, double base,

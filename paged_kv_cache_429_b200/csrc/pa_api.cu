@@ -815,6 +815,7 @@ pa_status pa_rope_frequencies(double *inv_freq_out, float *rope_scale_out, int r
     return PA_ERR_INVALID_ARG;
   const double r = rotary_dim, two_pi = 2.0 * std::acos(-1.0);
   if (scaling == PA_ROPE_BASE) base *= std::pow(factor, r / (r - 2.0));
+  if (!std::isfinite(base)) return PA_ERR_INVALID_ARG;
   // YaRN's ramp: the (real-valued) component that turns `turns` times in the
   // original context, N base^(-2i/r) / 2 pi = turns
   double lo = 0.0, hi = 1.0;

@@ -315,3 +315,11 @@ def test_binding_refuses_workspaces_that_hold_less_than_they_say():
     with pytest.raises(TypeError, match="torch.Tensor"):
         pa._need_workspace(np.empty(512, np.uint8), 0)
     pa._need_workspace(torch.empty(512, dtype=torch.uint8), -1)
+
+
+@pytest.mark.parametrize("r,base,factor", [(4, 10000.0, 1e153), (64, 1e300, 1e9), (6, 1e4, 1e250)])
+def test_a_stretched_base_past_64_bits_is_refused(r, base, factor):
+    with pytest.raises(pa.PagedAttentionError, match="PA_ERR_INVALID_ARG"):
+        pa.pa_rope_frequencies(r, base, pa.PA_ROPE_BASE, factor=factor)
+    inv, _ = pa.pa_rope_frequencies(r, 10000.0, pa.PA_ROPE_BASE, factor=1e100)
+    assert bool(torch.all(torch.isfinite(inv) & (inv > 0)))
