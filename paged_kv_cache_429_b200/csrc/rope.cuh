@@ -22,9 +22,9 @@
 // Together below 2^-23 radians + 2^-104 |t inv_freq|.
 //
 // What bounds it: DRAM for prompts (32768 tokens of 32 query and 8 KV heads
-// of 128, 806 MB, in 132 us: 0.93 of the copy bandwidth), the latency of a
-// launch, a load and a sincospi for a decode step (64 tokens of 32 and 32
-// heads 2.8 us, in a graph). Layout: a CTA takes a few tokens,
+// of 128, 806 MB, in 132 to 137 us: 0.90 to 0.93 of the copy bandwidth), the
+// latency of a launch, a load and a sincospi for a decode step (64 tokens of
+// 32 and 32 heads 2.5 us, in a graph). Layout: a CTA takes a few tokens,
 // computes each (token, pair)'s cosine and sine once into shared memory,
 // then moves units of 16 elements (two 16-byte loads, two stores): a pair
 // of partner chunks in the half layout, two neighbouring chunks in the

@@ -14,11 +14,12 @@
 // of the prefix and leaves records
 //     m (log2 units), l = sum 2^(z - m), o = sum 2^(z - m) V
 // in the workspace. The suffix kernel streams each sequence's own blocks as
-// the plain decode does, launched so that it fills the SMs as the prefix
-// kernel leaves them; its parts are records too. The join kernel adds up
-// each row's records. A sequence that ends inside its prefix takes its whole
-// context as its own part, so that no masked product ever meets a value it
-// must not see (0 * NaN).
+// the plain decode does, its CTAs started on the SMs as the prefix kernel
+// leaves them (each waits for that kernel's end before it merges, so an SM
+// takes one set of them until then); its parts are records too. The join
+// kernel adds up each row's records. A sequence that ends inside its prefix
+// takes its whole context as its own part, so that no masked product ever
+// meets a value it must not see (0 * NaN).
 //
 // The prefix kernel's CTA: two query tiles of 128 rows against at most 16
 // key tiles of 128, K and V by TMA (E4M3 bytes widened to f16 by a warpgroup
@@ -33,9 +34,10 @@
 // 32768 shared tokens: 104 us, 660 TFLOP/s of the formula's, 990 with the
 // second halves of the weights. The suffix kernel is bound by DRAM where
 // there is enough of it (256 sequences of 40 heads, 992 shared and up to 2048
-// own tokens: the whole call 2.58 GB in 400 us, 0.985 of the copy bandwidth);
-// short suffixes of few heads (130 sequences of 250 tokens, 8 heads, E4M3)
-// take 24 us against 10, the latency of a part's start and of its merge.
+// own tokens: the whole call 2.58 GB in 400 to 417 us, 0.95 to 0.985 of the
+// copy bandwidth); short suffixes of few heads (130 sequences of 250 tokens,
+// 8 heads, E4M3) take 24 us against 10, the latency of a part's start and of
+// its merge.
 //
 // Precision. The output is fp32, so the weights 2^(z - m) enter the value
 // product as two 16-bit halves (hi = round(p), lo = round(p - hi)): bf16

@@ -15,7 +15,7 @@
 // p = L_s + t - Q_s in slot table[s][p / 16] * 16 + p % 16.
 //
 // What bounds it. A decode step moves a few KB: the chain launch, lengths,
-// sums, ids, stores (3.1 us for 128 rows of one token, in a graph). A large
+// sums, ids, stores (3.2 us for 128 rows of one token, in a graph). A large
 // admission writes 12 bytes a token (4.7 us at the copy rate for 2.6 million
 // tokens of 2000 rows), but spends its time on issuing instructions, about
 // 100 a token: 16 us, of which the sums take 4. The two exclusive sums over the rows are
