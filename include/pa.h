@@ -222,7 +222,9 @@ PA_API pa_status pa_decode_no_alloc(float *out, const void *q, const void *k_cac
 
 /* Bytes of workspace pa_decode_shared_prefix needs for these arguments (0
  * for invalid ones): the partial outputs, maxima and sums of the prefixes
- * and, where the suffixes are split, of their partitions. */
+ * and, where the suffixes are split, of their partitions. A smaller batch is
+ * cut into more parts and can need more (up to 1.8 times): a workspace kept
+ * for several sizes is as large as the largest of theirs. */
 PA_API size_t pa_decode_shared_prefix_workspace_size(int num_seqs, int num_q_heads,
                                                      int num_kv_heads, int head_dim,
                                                      int num_groups,
