@@ -288,3 +288,34 @@ def test_large_frequencies_at_far_positions(interleaved):
     pa_rope_and_cache(out, q, k, v, kc, vc, slots, pos, inv, interleaved=interleaved)
     torch.cuda.synchronize()
     check(q, k, v, kc, vc, slots, pos, inv, 16, interleaved, 1.0, False, 1.0, 1.0, out, kc0)
+
+
+@pytest.mark.parametrize("tokens", [5, 1500])
+def test_offsets_past_32_bits(tokens):
+    """Slots past 2^31 elements of a cache, and tokens so far apart that the
+    last one starts past 2^31 elements of their tensor."""
+    hkv, d = 8, 128
+    nb = (1 << 31) // (hkv * B * d) + 200
+    kc = torch.zeros((nb, hkv, B, d), dtype=torch.bfloat16, device="cuda")
+    vc = torch.zeros_like(kc)
+    heads, stride = 16 + 2 * hkv, (1 << 31) // (tokens - 1) // 8 * 8 + 8
+    g = torch.Generator(device="cuda").manual_seed(61)
+    rows = torch.randn((tokens, heads, d), generator=g, device="cuda").to(torch.bfloat16)
+    far = torch.empty(stride * (tokens - 1) + heads * d, dtype=torch.bfloat16, device="cuda")
+    far = far.as_strided((tokens, heads, d), (stride, d, 1))
+    far.copy_(rows)
+    first = nb * B - 2 * tokens       # in the last blocks
+    slots = first + 2 * torch.randperm(tokens, generator=g, device="cuda")
+    pos = torch.arange(tokens, dtype=torch.int32, device="cuda")
+    inv, _ = pa_rope_frequencies(d, device="cuda")
+    out = torch.empty((tokens, 16, d), dtype=torch.bfloat16, device="cuda")
+    pa_rope_and_cache(out, far[:, :16], far[:, 16:16 + hkv], far[:, 16 + hkv:], kc, vc, slots, pos, inv)
+    torch.cuda.synchronize()
+    # the same tokens close together, into the cache's last blocks alone
+    low = first // B
+    k2, v2 = torch.zeros_like(kc[low:]), torch.zeros_like(vc[low:])
+    out2 = torch.empty_like(out)
+    pa_rope_and_cache(out2, rows[:, :16], rows[:, 16:16 + hkv], rows[:, 16 + hkv:], k2, v2, slots - low * B, pos, inv)
+    assert torch.equal(out, out2) and torch.equal(kc[low:], k2) and torch.equal(vc[low:], v2)
+    assert int(torch.count_nonzero(k2)) > 0 and int(torch.count_nonzero(kc[:low])) == 0
+    assert pa_get_device_error() == 0

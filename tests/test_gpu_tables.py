@@ -515,3 +515,56 @@ def test_large_releases_refuse_on_the_device(what, inplace):
     np.testing.assert_array_equal(lo.cpu().numpy(), wl)
     assert int(co) == wc
     assert pa_get_device_error() == flags
+
+
+def test_tables_of_more_than_2_to_31_entries():
+    """Rows that start past 2^31 entries of the table, one CTA and two launches."""
+    W = (1 << 27) - 9               # columns: just below the most
+    S = -(-(1 << 31) // W) + 2      # 19 rows, the last ones past 2^31
+    tables = torch.full((S, W), -1, dtype=torch.int32, device="cuda")
+    lens = np.zeros(S, np.int64)
+    lens[S - 1], lens[S - 2], lens[3] = 16 * (W - 200) + 5, 33, 1
+    tables[S - 2, :2] = 14
+    tables[S - 1, W - 200], tables[S - 2, 2], tables[3, 0] = 11, 12, 13
+    for new_tokens in (17, 2100):
+        new = np.zeros(S, np.int64)
+        new[S - 1], new[S - 2], new[3] = new_tokens, 20, 0
+        need = int((-(-(lens + new) // B) - -(-lens // B)).sum())
+        ln, fr, ct = dev(lens), dev(np.arange(100, 100 + need)), dev([need])
+        T = int(new.sum()) + 3
+        sl = torch.empty(T, dtype=torch.int64, device="cuda")
+        ps, qs = torch.empty(T, dtype=torch.int32, device="cuda"), torch.empty(S + 1, dtype=torch.int32, device="cuda")
+        pa_extend_tables(tables, ln, dev(new), fr, ct, ln, ct, sl, ps, qs, num_blocks=1000)
+        torch.cuda.synchronize()
+        assert pa_get_device_error() == 0 and int(ct) == 0
+        np.testing.assert_array_equal(ln.cpu().numpy(), lens + new)
+        stack, at, got = list(range(100, 100 + need)), 0, sl.cpu().numpy()
+        for s in range(S):
+            ids = {int(lens[s]) // B: {S - 1: 11, S - 2: 12, 3: 13}.get(s)}
+            for p in range(int(lens[s]), int(lens[s] + new[s])):
+                if p % B == 0:
+                    ids[p // B] = stack.pop()
+                    assert int(tables[s, p // B]) == ids[p // B]
+                assert got[at] == ids[p // B] * B + p % B and int(ps[at]) == p
+                at += 1
+        assert np.all(got[at:] == -1)
+        # and back: a small bound keeps every block but the row's last ones
+        rel = np.zeros(S, np.int64)
+        rel[S - 1] = 1
+        keep = int(lens[S - 1]) // B + 1
+        fr2, ct2, l2 = dev(np.full(need + 2, -7)), dev([1]), torch.empty_like(ln)
+        c2 = torch.empty_like(ct2)
+        pa_release_tables(tables, ln, dev(rel), fr2, ct2, l2, c2, keep_blocks=keep, num_blocks=1000)
+        torch.cuda.synchronize()
+        n = -(-int(lens[S - 1] + new[S - 1]) // B) - keep
+        assert int(c2) == 1 + n and pa_get_device_error() == 0
+        np.testing.assert_array_equal(fr2.cpu().numpy()[1:1 + n], tables[S - 1, keep:keep + n].cpu().numpy())
+        assert int(l2[S - 1]) == keep * B
+        # without a bound two launches; the row before, whole
+        rel[:] = 0
+        rel[S - 2] = 1
+        fr2, ct2 = dev(np.full(9, -7)), dev([2])
+        pa_release_tables(tables, ln, dev(rel), fr2, ct2, l2, c2, num_blocks=1000)
+        torch.cuda.synchronize()
+        assert int(c2) == 6 and int(l2[S - 2]) == 0 and pa_get_device_error() == 0
+        np.testing.assert_array_equal(fr2.cpu().numpy()[2:6], tables[S - 2, :4].cpu().numpy())
