@@ -477,3 +477,24 @@ def test_sequences_beside_overlapping_groups_are_right():
     torch.cuda.synchronize()
     assert pa_get_device_error() & GROUP
     b.check(out, subset=np.array([0, 1, 2, 9, 10, 11]))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("junk", [float("nan"), float("inf"), 3.0e38])
+def test_padded_rows_hold_anything(junk, fp8):
+    """Rows without tokens, in the middle of a group and behind the last one,
+    whose queries are what an earlier step left: zeros come out, and nothing
+    of them reaches the other rows of their tiles. A live row of such queries
+    spoils itself alone."""
+    b = Batch(16, 4, 128, [21, 9], [70, 25], suffixes(28, 34, 0, 60), fp8=fp8, seed=28, tail=4)
+    empty, spoilt = [3, 11, 20, 22, 31, 33], 7
+    b.lens[empty] = 0
+    b.q[empty] = junk
+    b.q[spoilt] = float("nan")
+    out = b.run()
+    torch.cuda.synchronize()
+    assert torch.count_nonzero(out[empty]) == 0 and bool(torch.isnan(out[spoilt]).all())
+    live = np.array([s for s in range(b.S) if s != spoilt])
+    b.q[empty + [spoilt]] = 1.0       # for the oracle and the tolerance
+    b.check(out, subset=live)
+    assert pa_get_device_error() == 0

@@ -568,3 +568,41 @@ def test_tables_of_more_than_2_to_31_entries():
         torch.cuda.synchronize()
         assert int(c2) == 6 and int(l2[S - 2]) == 0 and pa_get_device_error() == 0
         np.testing.assert_array_equal(fr2.cpu().numpy()[2:6], tables[S - 2, :4].cpu().numpy())
+
+
+def test_large_calls_captured_and_replayed():
+    """Both two-launch calls in place in one graph, other rows each time, a
+    refused step among them."""
+    g, tables, lens, free, count, nb = state(7, 600, 40, 60, nb_spare=30000)
+    t, ln, fr, ct = dev(tables), dev(lens), dev(free), dev([count])
+    T = 12000
+    sl = torch.empty(T, dtype=torch.int64, device="cuda")
+    ps, qs = torch.empty(T, dtype=torch.int32, device="cuda"), torch.empty(601, dtype=torch.int32, device="cuda")
+    new, rel = dev(np.zeros(600)), dev(np.zeros(600))
+
+    def step():
+        pa_extend_tables(t, ln, new, fr, ct, ln, ct, sl, ps, qs, num_blocks=nb)
+        pa_release_tables(t, ln, rel, fr, ct, ln, ct, num_blocks=nb)
+
+    step()                       # of nothing: loads the kernels
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i in range(6):
+        n, r = g.integers(0, 30, 600), (g.random(600) < 0.3).astype(np.int32)
+        if i == 3:
+            n[5] = 40 * B        # past its table
+        new.copy_(dev(n))
+        rel.copy_(dev(r))
+        graph.replay()
+        torch.cuda.synchronize()
+        tables, lens, count, slots, pos, start, flags = plain_extend(tables, lens, n, free, count, T, nb)
+        assert (flags == LENGTH) == (i == 3)
+        assert pa_get_device_error() == flags
+        free, lens, count, flags = plain_release(tables, lens, r, free, count, 0, nb)
+        assert flags == 0
+        for got, want in ((t, tables), (ln, lens), (sl, slots), (ps, pos), (qs, start), (ct, [count])):
+            np.testing.assert_array_equal(got.cpu().numpy(), want)
+        np.testing.assert_array_equal(fr.cpu().numpy()[:count], free[:count])
+    del graph
