@@ -222,9 +222,9 @@ PA_API pa_status pa_decode_no_alloc(float *out, const void *q, const void *k_cac
 
 /* Bytes of workspace pa_decode_shared_prefix needs for these arguments (0
  * for invalid ones): the partial outputs, maxima and sums of the prefixes
- * and, where the suffixes are split, of their partitions. A smaller batch is
- * cut into more parts and can need more (up to 1.8 times): a workspace kept
- * for several sizes is as large as the largest of theirs. */
+ * and, where the suffixes are split, of their partitions. A smaller batch can
+ * be cut into more parts and need more: a workspace kept for several sizes is
+ * as large as the largest of theirs. */
 PA_API size_t pa_decode_shared_prefix_workspace_size(int num_seqs, int num_q_heads,
                                                      int num_kv_heads, int head_dim,
                                                      int num_groups,
@@ -357,8 +357,9 @@ typedef enum {
  * (HOST) receives the angles per position in radians, *rope_scale_out (host)
  * the factor on the rotated values (1 except for PA_ROPE_YARN). rotary_dim:
  * a positive even number (above 2 for PA_ROPE_BASE, whose stretched base has
- * to be finite); base > 1; factor >= 1 (not read for NONE); original_max_position > 0 and 0 < low < high for
- * BANDS and YARN (not read otherwise). Anything else: PA_ERR_INVALID_ARG. */
+ * to be finite); base > 1; factor >= 1 (not read for NONE);
+ * original_max_position > 0 and 0 < low < high for BANDS and YARN (not read
+ * otherwise). Anything else: PA_ERR_INVALID_ARG. */
 PA_API pa_status pa_rope_frequencies(double *inv_freq_out, float *rope_scale_out,
                                      int rotary_dim, double base,
                                      pa_rope_scaling scaling, double factor,
